@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_HERE, "_build", "libfa.so")
 
 FA_OK = 0
 STATUS_NAMES = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED",
-                3: "FA_ERR_MISALIGNED", 4: "FA_ERR_CUDA", 5: "FA_ERR_TIMEOUT"}
+                3: "FA_ERR_MISALIGNED", 4: "FA_ERR_CUDA", 5: "FA_ERR_TIMEOUT",
+                6: "FA_ERR_BAD_INDEX"}
 
 FA_BF16, FA_F32, FA_F16 = 0, 1, 2
 _DTYPES = {torch.bfloat16: FA_BF16, torch.float32: FA_F32, torch.float16: FA_F16}
@@ -33,9 +34,16 @@ class FaTensor(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class FaCache(ctypes.Structure):
+    """struct fa_cache: a pool of pages holding K and V in 4 bits."""
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 # Every symbol include/fa.h declares, with its ctypes signature.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_tp = ctypes.POINTER(FaTensor)
+_tp, _cp, _i64 = ctypes.POINTER(FaTensor), ctypes.POINTER(FaCache), ctypes.c_int64
 SIGNATURES = {
     "fa_abi_version": ([], _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
@@ -55,6 +63,12 @@ SIGNATURES = {
                        [_i, _i, _i, _i, _i, _i, _f, _vp, _vp, _sz, _vp], _i),
     "fa_backward_noalloc": ([_vp] * 9 + [_i, _i, _i, _i, _i, _f, _vp, _vp], _i),
     "fa_backward_noalloc_max_bytes": ([], _sz),
+    "fa_cache_bytes": ([_i, _i, _i, _i], _sz),
+    "fa_cache_write": ([_cp, _tp, _tp, _vp, _i64, _i, _vp, _vp, _i, _i, _vp], _i),
+    "fa_cache_read": ([_cp, _tp, _tp, _vp, _i64, _i, _vp, _vp, _i, _i, _vp], _i),
+    "fa_cache_forward": ([_tp, _cp, _vp, _i64, _i, _vp, _vp, _tp, _vp, _i, _i, _i, _i, _f, _vp,
+                          _sz, _vp], _i),
+    "fa_cache_forward_workspace_bytes": ([_i, _i, _i, _i], _sz),
     "fa_device_status": ([_vp, ctypes.POINTER(ctypes.c_uint)], _i),
     "fa_debug_configure": ([ctypes.c_uint, ctypes.c_ulonglong], _i),
     "fa_num_kernels": ([], _i),
@@ -285,12 +299,174 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     return dq, dk, dv
 
 
+class KVCache4:
+    """A pool of pages holding keys and values in 4 bits (fa_cache).
+
+    ``num_pages`` pages of ``page_size`` tokens (a multiple of 16) for
+    ``heads`` key/value heads of dimension ``d`` (64, 96, 128 or 256). Rows of
+    K and V, and the queries that attend over them, are of ``dtype`` (bf16 or
+    fp16). A group of 32 channels x of a row is stored as lo = min x,
+    s = (max x - lo) / 15 and 4-bit u = round((x - lo) / s), 5 bits a channel
+    in all, and stands for lo + s u (include/fa.h has the rounding). ``data``
+    holds the pool's bytes, uninitialised; their arrangement is private to the
+    library.
+    """
+
+    def __init__(self, num_pages: int, heads: int, d: int, page_size: int = 64,
+                 dtype=torch.bfloat16, device=None):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"a cache holds bf16 or fp16 rows, not {dtype}")
+        nbytes = int(_lib_fast().fa_cache_bytes(num_pages, heads, page_size, d))
+        if nbytes == 0:
+            raise ValueError(f"no cache of {num_pages} pages, {heads} heads, d {d}, page size "
+                             f"{page_size}: the sizes are positive, d is 64, 96, 128 or 256 and "
+                             "the page size a multiple of 16")
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise ValueError(f"a cache lives on a CUDA device, not on {device}")
+        self.num_pages, self.heads, self.d, self.page_size = num_pages, heads, d, page_size
+        self.dtype = dtype
+        self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self._desc = FaCache(self.data.data_ptr(), num_pages, heads, page_size, d,
+                             _DTYPES[dtype], 0)
+
+
+def _ints(t, B, name, device):
+    """Pointer of an int32 CUDA tensor [B] (contiguous) or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != B or \
+            (B > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{B}] on {device}")
+    return t.data_ptr()
+
+
+def _table(page_table, B, device):
+    """(pointer, row stride, entries a row) of an int32 page table [B, pages]."""
+    if page_table.dtype != torch.int32 or page_table.device != device or \
+            page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1 or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be an int32 tensor [{B}, pages] on {device} with "
+                         "contiguous rows")
+    return page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
+
+
+def _cache_rows(fn, cache, k, v, page_table, start, counts):
+    ks = k.shape
+    if ks != v.shape or len(ks) != 4 or ks[1] != cache.heads or ks[3] != cache.d:
+        raise ValueError(f"k and v must be [B, {cache.heads}, N, {cache.d}]")
+    dev = cache.data.device
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on the cache's device {dev}")
+    B, _, N, _ = ks
+    if start is None:
+        raise ValueError("start must be an int32 tensor [B]")
+    table, stride, pages = _table(page_table, B, dev)
+    at, cnt = _ints(start, B, "start", dev), _ints(counts, B, "counts", dev)
+    _check(getattr(_lib_fast(), fn)(
+        cache._desc, _desc(k, "k"), _desc(v, "v"), table, stride, pages, at, cnt, B, N,
+        _stream(dev)), fn)
+
+
+def cache_write(cache: KVCache4, k, v, page_table, start, counts=None):
+    """Quantise rows of k and v into the cache as they are written.
+
+    k, v: [B, heads, N, d] of the cache's dtype, any strides over the first
+    three dimensions. Row i of sequence b becomes token ``start[b] + i``, for
+    i < ``counts[b]`` (all N without counts). ``page_table`` is int32
+    [B, pages]: token p of sequence b is token p % page_size of page
+    ``page_table[b, p // page_size]``. ``start`` and ``counts`` are int32 [B].
+    These tensors are read on the device, so a captured graph follows them. A
+    page or token out of range is skipped and reported by ``device_status``.
+    """
+    _cache_rows("fa_cache_write", cache, k, v, page_table, start, counts)
+
+
+def cache_read(cache: KVCache4, page_table, start, n: int, counts=None, k=None, v=None):
+    """k, v [B, heads, n, d]: what tokens ``start[b] + i``, i < n, stand for, rounded
+    to the cache's dtype; rows from ``counts[b]`` on are zeros. Arguments as
+    for ``cache_write``; ``k`` and ``v`` receive the rows if given."""
+    shape = (page_table.shape[0], cache.heads, n, cache.d)
+    k = torch.empty(shape, dtype=cache.dtype, device=cache.data.device) if k is None else k
+    v = torch.empty(shape, dtype=cache.dtype, device=cache.data.device) if v is None else v
+    if k.shape != shape or v.shape != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    _cache_rows("fa_cache_read", cache, k, v, page_table, start, counts)
+    return k, v
+
+
+def cache_forward(q, cache: KVCache4, page_table, lengths, causal: bool = False,
+                  scale: float | None = None, counts=None, out=None, lse=None, o_dtype=None,
+                  workspace=None):
+    """O, LSE = attention of q over what the cache stands for.
+
+    q: [B, Hq, Nq, d] of the cache's dtype, any strides over the first three
+    dimensions; query head h reads cached head h // (Hq // heads). Sequence b
+    holds ``lengths[b]`` tokens (int32 [B]); its query rows i < ``counts[b]``
+    (all Nq without counts) are its last counts[b] tokens, which the cache
+    already holds, and with ``causal`` each sees the tokens up to itself. Rows
+    that see no token, and rows from counts[b] on, get O = 0 and LSE = -inf.
+    O has q's shape, and q's layout and dtype unless ``out`` or
+    ``o_dtype=torch.float32`` say otherwise; LSE is fp32 contiguous
+    [B, Hq, Nq]. ``workspace``: a uint8 tensor of
+    ``cache_forward_workspace_bytes`` bytes for callers that keep one; calls
+    that may overlap need one each. Lengths, counts and the page table are read
+    on the device (see ``cache_write``).
+    """
+    qs = q.shape
+    if len(qs) != 4 or qs[3] != cache.d or qs[1] % cache.heads:
+        raise ValueError(f"q must be [B, Hq, Nq, {cache.d}] with Hq a multiple of {cache.heads}")
+    dev = cache.data.device
+    B, Hq, Nq, d = qs
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q, dtype=q.dtype if o_dtype is None else o_dtype)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    if out.shape != qs or lse.shape != (B, Hq, Nq) or \
+            lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("out must be [B, Hq, Nq, d] and lse contiguous fp32 [B, Hq, Nq]")
+    if q.device != dev or out.device != dev or lse.device != dev:
+        raise ValueError(f"q, out and lse must be on the cache's device {dev}")
+    if lengths is None:
+        raise ValueError("lengths must be an int32 tensor [B]")
+    table, stride, pages = _table(page_table, B, dev)
+    ln, cnt = _ints(lengths, B, "lengths", dev), _ints(counts, B, "counts", dev)
+    if workspace is None:
+        workspace = torch.empty(cache_forward_workspace_bytes(Hq, cache.heads, Nq, d, dev),
+                                dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, on the cache's device {dev}")
+    _check(_lib_fast().fa_cache_forward(
+        _desc(q, "q"), cache._desc, table, stride, pages, ln, cnt, _desc(out, "out"),
+        lse.data_ptr(), B, Hq, Nq, int(bool(causal)), scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(dev)), "fa_cache_forward")
+    return out, lse
+
+
+_cache_ws = {}
+
+
+def cache_forward_workspace_bytes(Hq, Hk, Nq, d, device=None) -> int:
+    """Workspace bytes of ``cache_forward`` on ``device`` (default: the current CUDA
+    device), whatever the batch and the lengths."""
+    idx = torch.device(device).index if device is not None else None
+    idx = torch.cuda.current_device() if idx is None else idx
+    n = _cache_ws.get((idx, Hq, Hk, Nq, d))
+    if n is None:
+        with torch.cuda.device(idx):
+            n = int(_lib_fast().fa_cache_forward_workspace_bytes(Hq, Hk, Nq, d))
+        _cache_ws[(idx, Hq, Hk, Nq, d)] = n
+    return n
+
+
 def device_status(stream=None) -> int:
-    """Synchronise and read/clear the device status word (0 = no wait gave up)."""
+    """Synchronise and read/clear the device status word (0: no wait gave up and no index
+    was out of range)."""
     code = ctypes.c_uint(0)
     st = _stream() if stream is None else ctypes.c_void_p(stream)
     rc = load_library().fa_device_status(st, ctypes.byref(code))
-    if rc not in (FA_OK, 5):
+    if rc not in (FA_OK, 5, 6):
         raise FAError(rc, "fa_device_status")
     return int(code.value)
 

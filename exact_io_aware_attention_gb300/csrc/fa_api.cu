@@ -15,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/fa.h"
+#include "fa_cache.cuh"
 #include "fa_internal.h"
 
 namespace {
@@ -491,6 +492,184 @@ fa_tensor contiguous(const void *data, int H, int N, int d, int dtype) {
   return t;
 }
 
+// ---- the 4-bit K/V cache ------------------------------------------------------
+
+// Tokens a row of a page table may cover; keeps the attention kernel's
+// per-sequence work counts in 32 bits.
+constexpr long long kMaxCacheTokens = 1LL << 24;
+
+bool cache_sizes_ok(int num_pages, int heads, int page_size, int d) {
+  return num_pages >= 1 && heads >= 1 && page_size >= fa::kCellTokens &&
+         page_size % fa::kCellTokens == 0 && page_size <= kMaxCacheTokens &&
+         (d == 64 || d == 96 || d == 128 || d == 256);
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks a cache handle and the page table of a call and describes both to
+// the kernels.
+fa_status cache_pool(const fa_cache *c, const int32_t *table, int64_t table_stride, int max_pages,
+                     int B, fa::CachePool *out) {
+  if (!c || !c->data || !table) {
+    snprintf(g_last_error, sizeof(g_last_error), "cache: null cache or page table");
+    return FA_ERR_INVALID_ARG;
+  }
+  if (c->reserved != 0) {
+    snprintf(g_last_error, sizeof(g_last_error), "cache: reserved field is not 0");
+    return FA_ERR_INVALID_ARG;
+  }
+  if (c->num_pages < 1 || c->heads < 1 || c->page_size < 1 || max_pages < 1 ||
+      (B > 1 && (table_stride < 0 || table_stride >= (1LL << 40)))) {
+    snprintf(g_last_error, sizeof(g_last_error),
+             "cache: %d pages of %d tokens, %d heads, table of %d pages a row with stride %lld",
+             c->num_pages, c->page_size, c->heads, max_pages, (long long)table_stride);
+    return FA_ERR_INVALID_ARG;
+  }
+  if (!cache_sizes_ok(c->num_pages, c->heads, c->page_size, c->d) ||
+      (c->dtype != FA_BF16 && c->dtype != FA_F16)) {
+    snprintf(g_last_error, sizeof(g_last_error),
+             "cache: page size %d, d %d, dtype %d unsupported (a multiple of %d; 64, 96, 128 or "
+             "256; bf16 or f16)",
+             c->page_size, c->d, c->dtype, fa::kCellTokens);
+    return FA_ERR_UNSUPPORTED;
+  }
+  if ((long long)max_pages * c->page_size > kMaxCacheTokens) {
+    snprintf(g_last_error, sizeof(g_last_error),
+             "cache: a table row of %d pages of %d tokens covers more than %lld tokens", max_pages,
+             c->page_size, kMaxCacheTokens);
+    return FA_ERR_UNSUPPORTED;
+  }
+  if (!aligned16(c->data) || !aligned4(table)) {
+    snprintf(g_last_error, sizeof(g_last_error),
+             "cache: data %p is not 16-byte aligned or page table %p not 4-byte aligned", c->data,
+             (const void *)table);
+    return FA_ERR_MISALIGNED;
+  }
+  out->data = static_cast<uint8_t *>(c->data);
+  out->table = table;
+  out->table_stride = B > 1 ? table_stride : 0;
+  out->num_pages = c->num_pages;
+  out->heads = c->heads;
+  out->page_cells = c->page_size / fa::kCellTokens;
+  out->table_cells = max_pages * out->page_cells;
+  out->d = c->d;
+  out->f16 = c->dtype == FA_F16 ? 1 : 0;
+  return FA_OK;
+}
+
+fa_status cache_rows_impl(const fa_cache *cache, const fa_tensor *K, const fa_tensor *V,
+                          const int32_t *table, int64_t table_stride, int max_pages,
+                          const int32_t *start, const int32_t *counts, int B, int N, bool write,
+                          void *stream) {
+  if (B < 0 || N < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return FA_OK;
+  fa::CacheRowsParams p;
+  memset(&p, 0, sizeof(p));
+  fa_status s = cache_pool(cache, table, table_stride, max_pages, B, &p.pool);
+  if (s != FA_OK) return s;
+  if (!K || !V || !start) return FA_ERR_INVALID_ARG;
+  if ((double)B * cache->heads * N > 2147483647.0) return FA_ERR_UNSUPPORTED;
+  if (!aligned4(start) || !aligned4(counts)) return FA_ERR_MISALIGNED;
+  if ((s = check_dtype(K, cache->dtype, false, "K")) != FA_OK ||
+      (s = check_dtype(V, cache->dtype, false, "V")) != FA_OK ||
+      (s = operand_strides(K, B, cache->heads, N, cache->d, 2, "K", &p.sk)) != FA_OK ||
+      (s = operand_strides(V, B, cache->heads, N, cache->d, 2, "V", &p.sv)) != FA_OK ||
+      (s = bind_device(cache->data)) != FA_OK)
+    return s;
+  p.start = start;
+  p.counts = counts;
+  p.k = K->data;
+  p.v = V->data;
+  p.B = B;
+  p.n = N;
+  cudaError_t e = status_word(&p.status);
+  if (e != cudaSuccess) return cuda_fail("cudaGetSymbolAddress", e);
+  NvtxRange range(write ? "fa_cache_write" : "fa_cache_read");
+  e = write ? fa::launch_cache_write(p, static_cast<cudaStream_t>(stream))
+            : fa::launch_cache_read(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(write ? "cache write launch" : "cache read launch", e);
+}
+
+// Scratch of the attention over a cache: two partial results (fp32 O rows and
+// log2-sum-exp) and one chain record per CTA of a full GPU.
+struct CacheScratch {
+  int ctas;
+  size_t part, lse, chain;
+};
+bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, CacheScratch *out) {
+  if (sms <= 0 || Hk <= 0) return false;
+  const int nt = fa::cache_forward_row_tiles(d, (long long)(Hq / Hk) * Nq);
+  out->ctas = sms * fa::cache_forward_ctas_per_sm(d, nt);
+  const size_t rows = (size_t)out->ctas * 2 * 8 * nt;
+  out->part = round_up(rows * d * sizeof(float));
+  out->lse = round_up(rows * sizeof(float));
+  out->chain = round_up((size_t)out->ctas * sizeof(int4));
+  return true;
+}
+
+fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const int32_t *table,
+                             int64_t table_stride, int max_pages, const int32_t *lengths,
+                             const int32_t *counts, const fa_tensor *O, float *LSE, int B, int Hq,
+                             int Nq, int causal, float scale, void *workspace, size_t ws_bytes,
+                             void *stream) {
+  if (B < 0 || Hq < 0 || Nq < 0) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (B == 0 || Hq == 0 || Nq == 0) return FA_OK;
+  fa::CacheFwdParams p;
+  memset(&p, 0, sizeof(p));
+  fa_status s = cache_pool(cache, table, table_stride, max_pages, B, &p.pool);
+  if (s != FA_OK) return s;
+  if (!Q || !O || !LSE || !lengths || !workspace) return FA_ERR_INVALID_ARG;
+  if (Hq % cache->heads != 0) {
+    snprintf(g_last_error, sizeof(g_last_error), "%d query heads over %d cached heads", Hq,
+             cache->heads);
+    return FA_ERR_INVALID_ARG;
+  }
+  const int d = cache->d;
+  if ((double)B * Hq * Nq > 1073741823.0) return FA_ERR_UNSUPPORTED;
+  const int o_bytes = O->dtype == FA_F32 ? 4 : 2;
+  if ((s = check_dtype(Q, cache->dtype, false, "Q")) != FA_OK ||
+      (s = check_dtype(O, cache->dtype, true, "O")) != FA_OK ||
+      (s = operand_strides(Q, B, Hq, Nq, d, 2, "Q", &p.sq)) != FA_OK ||
+      (s = operand_strides(O, B, Hq, Nq, d, o_bytes, "O", &p.so)) != FA_OK)
+    return s;
+  if (!aligned16(LSE) || !aligned4(lengths) || !aligned4(counts) ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return FA_ERR_MISALIGNED;
+  if ((s = bind_device(cache->data)) != FA_OK) return s;
+  CacheScratch w;
+  if (!cache_scratch(sm_count(), Hq, cache->heads, Nq, d, &w))
+    return cuda_fail("SM count", cudaErrorInvalidDevice);
+  if (ws_bytes < w.part + w.lse + w.chain) {
+    snprintf(g_last_error, sizeof(g_last_error), "workspace of %zu bytes, %zu needed", ws_bytes,
+             w.part + w.lse + w.chain);
+    return FA_ERR_INVALID_ARG;
+  }
+  p.lengths = lengths;
+  p.counts = counts;
+  p.q = Q->data;
+  p.o = O->data;
+  p.lse = LSE;
+  p.o_f32 = O->dtype == FA_F32 ? 1 : 0;
+  p.B = B;
+  p.hq = Hq;
+  p.group = Hq / cache->heads;
+  p.nq = Nq;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+  p.part = static_cast<float *>(workspace);
+  p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.part);
+  p.chain = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + w.part + w.lse);
+  p.ctas = w.ctas;
+  p.debug_flags = g_debug_flags.load();
+  p.wait_limit_ns = g_wait_limit_ns.load() ? g_wait_limit_ns.load() : fa::kWaitLimitNs;
+  cudaError_t e = status_word(&p.status);
+  if (e != cudaSuccess) return cuda_fail("cudaGetSymbolAddress", e);
+  NvtxRange range("fa_cache_forward");
+  e = fa::launch_cache_forward(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("cache forward launch", e);
+}
+
 // ---- measurement hooks ------------------------------------------------------
 
 struct ProbeRecord {
@@ -601,6 +780,10 @@ const char *fa_kernel_name(int kind) {
     case fa::kKindBwd256Dq: return "fa_bwd256_dq";
     case fa::kKindBwdFused: return "fa_bwd_fused";
     case fa::kKindBwdConvert: return "fa_bwd_dq_convert";
+    case fa::kKindCacheWrite: return "fa_cache_write";
+    case fa::kKindCacheRead: return "fa_cache_read";
+    case fa::kKindCacheFwd: return "fa_cache_fwd";
+    case fa::kKindCacheCombine: return "fa_cache_combine";
     default: return "";
   }
 }
@@ -645,6 +828,7 @@ const char *fa_status_string(int status) {
     case FA_ERR_MISALIGNED: return "FA_ERR_MISALIGNED";
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
+    case FA_ERR_BAD_INDEX: return "FA_ERR_BAD_INDEX";
     default: return "FA_ERR_UNKNOWN";
   }
 }
@@ -748,6 +932,42 @@ fa_status fa_backward_ex(const fa_tensor *Q, const fa_tensor *K, const fa_tensor
                        block_mask, workspace, workspace_bytes, stream);
 }
 
+size_t fa_cache_bytes(int num_pages, int heads, int page_size, int d) {
+  if (!cache_sizes_ok(num_pages, heads, page_size, d)) return 0;
+  return (size_t)num_pages * heads * (page_size / fa::kCellTokens) * fa::cell_bytes(d);
+}
+
+fa_status fa_cache_write(const fa_cache *cache, const fa_tensor *K, const fa_tensor *V,
+                         const int32_t *page_table, int64_t table_stride, int max_pages,
+                         const int32_t *start, const int32_t *counts, int B, int N,
+                         void *stream) {
+  return cache_rows_impl(cache, K, V, page_table, table_stride, max_pages, start, counts, B, N,
+                         true, stream);
+}
+
+fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tensor *V,
+                        const int32_t *page_table, int64_t table_stride, int max_pages,
+                        const int32_t *start, const int32_t *counts, int B, int N,
+                        void *stream) {
+  return cache_rows_impl(cache, K, V, page_table, table_stride, max_pages, start, counts, B, N,
+                         false, stream);
+}
+
+size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d) {
+  if (Hq < 0 || Hk <= 0 || Nq < 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
+  CacheScratch w;
+  return cache_scratch(sm_count(), Hq, Hk, Nq, d, &w) ? w.part + w.lse + w.chain : 0;
+}
+
+fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,
+                           int64_t table_stride, int max_pages, const int32_t *lengths,
+                           const int32_t *counts, const fa_tensor *O, float *LSE, int B, int Hq,
+                           int Nq, int causal, float scale, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  return cache_forward_impl(Q, cache, page_table, table_stride, max_pages, lengths, counts, O, LSE,
+                            B, Hq, Nq, causal, scale, workspace, workspace_bytes, stream);
+}
+
 fa_status fa_device_status(void *stream, unsigned int *code) {
   if (!code) return FA_ERR_INVALID_ARG;
   *code = 0;
@@ -760,7 +980,8 @@ fa_status fa_device_status(void *stream, unsigned int *code) {
   if (w && (e = cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero))) != cudaSuccess)
     return cuda_fail("cudaMemcpyToSymbol", e);
   *code = w;
-  return w ? FA_ERR_TIMEOUT : FA_OK;
+  if (!w) return FA_OK;
+  return (w & fa::kIndexBit) ? FA_ERR_BAD_INDEX : FA_ERR_TIMEOUT;
 }
 
 const char *fa_last_error(void) { return g_last_error; }

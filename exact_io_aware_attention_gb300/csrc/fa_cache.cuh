@@ -1,0 +1,154 @@
+// Layout of the 4-bit K/V cache (fa_cache in include/fa.h), shared by the
+// kernels that write it, read it back and attend over it.
+//
+// The pool is [num_pages][heads][page_size / 16] cells. A cell holds 16
+// consecutive tokens of one head and is contiguous (20 d bytes), so one bulk
+// copy brings a cell, or a run of cells of a page, into shared memory:
+//
+//   offset 0      K codes   16 rows of d/2 bytes
+//          8 d    V codes   16 rows of d/2 bytes
+//          16 d   K groups  16 rows of d/32 words: s (low half), lo (high half)
+//          18 d   V groups  likewise
+//
+// Within a cell the order of rows and nibbles is that of the registers of the
+// 16x8x16 matrix product the attention kernel runs on a cell, so a thread
+// reads its operands as whole words without bank conflicts and one AND turns
+// a word into two f16 operands: 4 bits in the low mantissa bits of an f16 are
+// the subnormal u * 2^-24 (u * 2^-20 one nibble up), exact in the product.
+//
+//   token j of a cell is matrix row cell_slot(j); K codes and both group
+//   arrays are in slot order, V codes in token order;
+//   K: channel c = 32 g + 8 t + i is nibble i/2 of the (i%2)-th half of word
+//   (t, g): the halves are the two k-neighbours of the product;
+//   V: channel c = 32 g + 4 r + i is nibble i of halfword (r, g): the
+//   k-neighbours are two tokens, paired up by a byte permute when read.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+constexpr int kCellTokens = 16;
+
+__host__ __device__ constexpr int cell_bytes(int d) { return 20 * d; }
+__host__ __device__ constexpr int cell_v_codes(int d) { return 8 * d; }
+__host__ __device__ constexpr int cell_k_groups(int d) { return 16 * d; }
+__host__ __device__ constexpr int cell_v_groups(int d) { return 18 * d; }
+
+// Matrix row of token j, and the token of matrix row s: the tokens of the
+// four thread columns t of a V operand (slots 2t, 2t+1, 2t+8, 2t+9) are t,
+// t + 4, t + 8 and t + 12, which lie in different banks.
+__host__ __device__ constexpr int cell_slot(int j) {
+  return ((j & 3) << 1) | ((j >> 2) & 1) | (j & 8);
+}
+__host__ __device__ constexpr int cell_token(int s) {
+  return ((s >> 1) & 3) | ((s & 1) << 2) | (s & 8);
+}
+
+// Byte offset of K's code word (slot, t, g) in a cell: 8 channels. For d = 256
+// the two 64-byte halves of a row (groups 0-3, 4-7) swap places in odd slots.
+template <int D>
+__host__ __device__ constexpr int k_word(int slot, int t, int g) {
+  return D == 256 ? slot * 128 + (((g >> 2) ^ (slot & 1)) << 6) + t * 16 + (g & 3) * 4
+                  : slot * (D / 2) + (t * (D / 32) + g) * 4;
+}
+
+// Byte offset of the first V word that thread row r reads of token j, and of
+// halfword (j, r, g): 4 channels of one group. Groups are paired in words
+// (two words a thread for d = 128, four for d = 256; the last group of d = 96
+// follows as halfwords); the order of the threads' pieces depends on the
+// token so that four consecutive tokens lie in different banks.
+template <int D>
+__host__ __device__ constexpr int v_piece(int j, int r) {
+  return cell_v_codes(D) + j * (D / 2) +
+         (D == 256   ? (r ^ ((j & 3) << 1)) * 16
+          : D == 128 ? (r ^ ((j & 2) << 1)) * 8
+                     : r * 4);
+}
+template <int D>
+__host__ __device__ constexpr int v_half(int j, int r, int g) {
+  return D == 96 && g == 2 ? cell_v_codes(D) + j * (D / 2) + 32 + r * 2 : v_piece<D>(j, r) + g * 2;
+}
+
+// Byte offset of the group word (s, lo) of a slot.
+template <int D>
+__host__ __device__ constexpr int k_group(int slot, int g) {
+  return cell_k_groups(D) + slot * (D / 8) + g * 4;
+}
+template <int D>
+__host__ __device__ constexpr int v_group(int slot, int g) {
+  return cell_v_groups(D) + slot * (D / 8) + g * 4;
+}
+
+// The pool and the page table of a call. Cell c of sequence b and head h (its
+// tokens 16 c .. 16 c + 15) is cell_ptr(page, h, c % page_cells), page =
+// table[b * table_stride + c / page_cells].
+struct CachePool {
+  uint8_t *data;
+  const int32_t *table;
+  long long table_stride;
+  int num_pages, heads, page_cells;   // page_cells = page_size / 16
+  int table_cells;                    // cells a row of the table covers
+  int d, f16;
+  __device__ __forceinline__ bool page_ok(int page) const {
+    return (unsigned)page < (unsigned)num_pages;
+  }
+  template <int D>
+  __device__ __forceinline__ uint8_t *cell_ptr(int page, int h, int in_page) const {
+    return data + (((size_t)page * heads + h) * page_cells + in_page) * (size_t)cell_bytes(D);
+  }
+};
+
+// Writing n rows of each (b, head) into the cache, or reading them back: row i
+// of sequence b is token start[b] + i, for i < counts[b] (n without counts).
+struct CacheRowsParams {
+  CachePool pool;
+  const int32_t *start, *counts;
+  void *k, *v;                        // 16-bit rows, strides sk / sv
+  RowStrides sk, sv;
+  int B, n;
+  unsigned int *status;
+};
+
+// Attention over the cache. Query row (b, hq, i), i < counts[b] (nq without
+// counts), is token lengths[b] - counts[b] + i of sequence b.
+struct CacheFwdParams {
+  CachePool pool;
+  const int32_t *lengths, *counts;
+  const void *q;                      // 16-bit rows, strides sq
+  RowStrides sq;
+  void *o;                            // 16-bit or fp32 rows, strides so
+  RowStrides so;
+  float *lse;                         // [B][Hq][nq]
+  int o_f32;
+  int B, hq, group, nq, causal;       // group = hq / heads of the pool
+  float scale_log2;
+  float *part;                        // scratch: [ctas][2][rows][d] partial outputs,
+  float *part_lse;                    // [ctas][2][rows] their log2-sum-exp,
+  int4 *chain;                        // [ctas] where a segment's parts lie
+  int ctas;                           // CTAs of the attention kernel
+  unsigned int *status;
+  uint32_t debug_flags;
+  uint64_t wait_limit_ns;
+};
+
+cudaError_t launch_cache_write(const CacheRowsParams &p, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheRowsParams &p, cudaStream_t stream);
+cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream);
+
+// Query rows (new tokens times query heads of one K/V head) that one CTA of
+// the attention kernel holds, in tiles of 8, the columns of its product: one
+// tile where that holds them all, else two (one for d = 256, whose outputs
+// would not fit the registers).
+constexpr int cache_forward_row_tiles(int d, long long rows) {
+  return d == 256 || rows <= 8 ? 1 : 2;
+}
+// CTAs of the attention kernel that one SM holds (its registers allow).
+constexpr int cache_forward_ctas_per_sm(int d, int row_tiles) {
+  return row_tiles == 1 ? (d == 256 ? 2 : d == 128 ? 3 : 4) : (d == 64 ? 3 : 2);
+}
+
+}  // namespace fa

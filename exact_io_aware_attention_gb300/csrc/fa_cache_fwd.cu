@@ -1,0 +1,761 @@
+// Attention over the 4-bit K/V cache: O = softmax(scale Q K^T) V where row j
+// of K and V is lo_j + s_j u_j per group of 32 channels.
+//
+// Mathematics. The groups' s and lo stay out of the matrix products:
+//     q . k_j = sum_g  s_jg (sum_{c in g} q_c u_jc) + lo_jg (sum_{c in g} q_c)
+//     o_c     = sum_j (p_j s_jg) u_jc  +  sum_j p_j lo_jg          (c in g)
+// so the operands of the products are the bare codes u, which an AND turns
+// into f16 subnormals u * 2^-24 (or u * 2^-20: the query channels and the
+// outputs concerned carry the factor), and s, lo are applied in fp32 to the
+// small side: 16 tokens x 8 query rows. The products run S^T = U Q^T and
+// O^T = U^T P^T with the tokens and the channels in the 16 rows of an m16n8k16
+// product and the query rows in its 8 columns, since a decoding step has few
+// query rows (the query heads of one K/V head times the new tokens).
+//
+// Why register operands and not tcgen05: a decoding step reads each code once
+// for at most 16 query rows, so HBM bounds it, and a tcgen05 operand would
+// have to pass through shared memory again as 16-bit values, four times the
+// bytes; mma.sync takes the expanded codes from the registers they are
+// expanded in.
+//
+// Numbers. Q is scaled per row by a power of two and converted to f16
+// (exactly, down to 2^-24 of the row's largest element). P s is rounded to
+// f16 (2^-11 relative); so that it neither overflows nor underflows whatever
+// the size of V, the running reference m of the softmax follows
+// max_j (score_j + log2 s_j) and not the maximum score. Sums, m, l and the lo
+// terms are fp32. m moves only when p s would pass 2^8 (the result does not
+// depend on m), so that a cell costs a vote and no reduction.
+//
+// Work. The cells of a (query block, K/V head) are one segment; all segments
+// lie end to end on one axis, in units of four cells, and every CTA takes an
+// equal share of it, whatever the lengths. A CTA's four warps take every
+// fourth cell, each with its own ring of bulk copies and its own m, l and O,
+// merged when the CTA leaves the segment. A segment within one CTA's share is
+// written out at once; parts of a segment go to scratch and
+// fa_cache_combine_kernel merges them in the order of the axis: the results
+// do not depend on timing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "fa_cache.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMinShare = 2;       // units of a CTA at least
+constexpr float kNoMax = -1e30f;   // m before the first visible key
+constexpr float kMinStep = 0x1p-24f, kMaxStep = 0x1p100f;  // s as m sees it
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Ring of a warp: cells in flight. About 50 KB a CTA, 150-200 KB an SM: the
+// bytes in flight that HBM's latency needs.
+template <int D>
+constexpr int kStages = D == 256 ? 4 : D == 128 ? 5 : D == 96 ? 7 : 10;
+
+template <int D, int NT>
+struct Layout {
+  static constexpr int kRing = kStages<D> * cell_bytes(D);
+  static constexpr int kOutPitch = D + 4;  // floats: rows 4 banks apart
+  static constexpr int kOut = 8 * NT * kOutPitch * 4;  // a warp's outputs reuse its ring
+  static constexpr int kWarp = ((kRing > kOut ? kRing : kOut) + 127) / 128 * 128;
+  static constexpr int kBars = kWarps * kWarp;                      // [warp][stage] mbarriers
+  static constexpr int kOk = kBars + kWarps * kStages<D> * 8;        // [warp][stage] page found
+  static constexpr int kStat = kOk + kWarps * kStages<D> * 4;        // [warp][8 NT] m, then l
+  static constexpr int kMisc = kStat + 2 * kWarps * 8 * NT * 4;      // scan and flags
+  static constexpr int kBytes = kMisc + 128;
+  static_assert(kBars % 8 == 0 && kMisc % 16 == 0, "alignment");
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8x8 matrix of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void lds64(uint32_t a, uint32_t &x, uint32_t &y) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t &x, uint32_t &y, uint32_t &z,
+                                       uint32_t &w) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// kN consecutive words; the address is aligned to the widest load that fits.
+template <int kN>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *w) {
+  if constexpr (kN == 2) {
+    lds64(a, w[0], w[1]);
+  } else if constexpr (kN == 3) {
+    w[0] = lds32(a);
+    w[1] = lds32(a + 4);
+    w[2] = lds32(a + 8);
+  } else {
+    lds128(a, w[0], w[1], w[2], w[3]);
+    if constexpr (kN == 8) lds128(a + 16, w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Query blocks on the work axis: block x = (sequence b, row block rb) has
+// `heads` segments of tiles(x) units each.
+struct Blocks {
+  const CacheFwdParams &p;
+  int row_blocks, rows;  // rows: query rows of a block
+
+  // New tokens, length and visible keys of block x. A length or count out of
+  // range is clamped (and recorded by `note`).
+  __device__ __forceinline__ void shape(int x, int &n, int &len, int &vis, bool note) const {
+    const int b = x / row_blocks, rb = x - b * row_blocks;
+    len = p.lengths[b];
+    n = p.counts ? p.counts[b] : p.nq;
+    const int cap = p.pool.table_cells * kCellTokens;
+    if (note && (len < 0 || len > cap || n < 0 || n > p.nq))
+      atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 3));
+    len = min(max(len, 0), cap);
+    n = min(max(n, 0), p.nq);
+    const int first = rb * rows / p.group;  // first new token of the block
+    const int last = min((rb * rows + rows - 1) / p.group, n - 1);
+    vis = first >= n ? 0 : p.causal ? min(len, max(len - n + last + 1, 0)) : len;
+  }
+  // A segment without visible keys has one unit too: its rows are written.
+  __device__ __forceinline__ int tiles(int vis) const {
+    return max(1, (vis + kWarps * kCellTokens - 1) / (kWarps * kCellTokens));
+  }
+};
+
+template <int D, int NT, bool kF16>
+__global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
+    fa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+  using L = Layout<D, NT>;
+  constexpr int kG = D / 32, kNs = kStages<D>, kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, t = lane & 3;
+  const uint32_t ring = sbase + warp * L::kWarp;
+  const uint32_t bars = sbase + L::kBars + warp * kNs * 8;
+  volatile int *const ok_flag = reinterpret_cast<int *>(smem + L::kOk) + warp * kNs;
+  float *const stat = reinterpret_cast<float *>(smem + L::kStat);
+  // [0] abort, [4..7] scan, [8..13] the block of the next piece: number, new
+  // tokens, length, visible keys, begin (64 bits)
+  int *const misc = reinterpret_cast<int *>(smem + L::kMisc);
+  const StatusSlot st = {p.status, misc, p.wait_limit_ns};
+
+  if (lane == 0)
+    for (int s = 0; s < kNs; ++s) mbar_init(bars + s * 8, 1);
+  if (threadIdx.x == 0) misc[0] = 0;
+  fence_mbar_init();
+
+  const Blocks blocks{p, (p.nq * p.group + kRows - 1) / kRows, kRows};
+  const int n_blocks = p.B * blocks.row_blocks, heads = p.pool.heads;
+
+  // This CTA's share [f, f_end) of the axis: the total, then the block in
+  // which f lies, by block-wide scans over the blocks' sizes. Everything that
+  // decides which piece comes next is read once and handed to all threads
+  // through shared memory: they agree even on values that change under the
+  // kernel.
+  long long total = 0;
+  for (int x0 = 0; x0 < n_blocks; x0 += kThreads) {
+    const int x = x0 + threadIdx.x;
+    int n, len, vis, size = 0;
+    if (x < n_blocks) {
+      blocks.shape(x, n, len, vis, blockIdx.x == 0);
+      size = blocks.tiles(vis);
+    }
+    size = __reduce_add_sync(0xffffffffu, size);
+    if (lane == 0) misc[4 + warp] = size;
+    __syncthreads();
+    total += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
+    __syncthreads();
+  }
+  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
+  long long f = share * blockIdx.x;
+  const long long f_end = min(f + share, total);
+  int4 chain = make_int4(-1, 0, 0, 0);
+  bool found = false;
+  for (long long x0 = 0, at0 = 0; x0 < n_blocks && f < f_end && !found; x0 += kThreads) {
+    const int x = int(x0) + threadIdx.x;
+    int n = 0, len = 0, vis = 0, size = 0;
+    if (x < n_blocks) {
+      blocks.shape(x, n, len, vis, false);
+      size = blocks.tiles(vis);
+    }
+    int incl = size;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) misc[4 + warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += misc[4 + w];
+    const long long at = at0 + (long long)(before + incl - size) * heads;
+    if (size > 0 && f >= at && f < at + (long long)size * heads) {
+      misc[8] = x;
+      misc[9] = n;
+      misc[10] = len;
+      misc[11] = vis;
+      *reinterpret_cast<long long *>(misc + 12) = at;
+    }
+    at0 += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
+    __syncthreads();
+    found = f < at0;
+  }
+
+  uint32_t fills = 0;  // cells this warp has consumed over all pieces: ring position and parity
+  bool first_piece = true;
+  while (found && f < f_end) {
+    // ---- the piece: units [t0, t1) of a segment --------------------------
+    const int blk = misc[8], n = misc[9], len = misc[10], vis = misc[11];
+    const long long blk_at = *reinterpret_cast<long long *>(misc + 12);
+    const int tiles = blocks.tiles(vis);
+    const int h = int((f - blk_at) / tiles);
+    if (h < 0 || h >= heads) break;
+    const long long seg_at = blk_at + (long long)h * tiles;
+    const int t0 = int(f - seg_at);
+    const int t1 = int(min((long long)tiles, f_end - seg_at));
+    const int b = blk / blocks.row_blocks, row0 = (blk - b * blocks.row_blocks) * kRows;
+    const int cells = (vis + kCellTokens - 1) / kCellTokens;
+    // this warp's cells: c0 + 4 k, k < nk
+    const int c0 = t0 * kWarps + warp;
+    const int c_end = min(t1 * kWarps, cells);
+    const int nk = c0 < c_end ? (c_end - c0 + kWarps - 1) / kWarps : 0;
+
+    // Page of cell k: lane k % 32 looks up the pages of 32 cells at a time,
+    // one batch ahead.
+    const int32_t *const table = p.pool.table + (size_t)((long long)b * p.pool.table_stride);
+    auto page_of = [&](int k) {
+      return k < nk ? table[(c0 + kWarps * k) / p.pool.page_cells] : 0;
+    };
+    int pages = page_of(lane), pages_next = page_of(32 + lane);
+    int issued = 0;
+    auto issue = [&]() {
+      const int k = issued;
+      if ((k & 31) == 0 && k > 0) {
+        pages = pages_next;
+        pages_next = page_of(k + 32 + lane);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, k & 31);
+      if (lane == 0 && !(p.debug_flags & kDebugSkipLoads)) {
+        const uint32_t s = (fills + k) % kNs;
+        const int c = c0 + kWarps * k;
+        const bool ok = p.pool.page_ok(page);
+        ok_flag[s] = ok;
+        if (ok) {
+          mbar_arrive_expect_tx(bars + s * 8, cell_bytes(D));
+          bulk_load_1d(ring + s * cell_bytes(D),
+                       p.pool.template cell_ptr<D>(page, h, c % p.pool.page_cells), cell_bytes(D),
+                       bars + s * 8);
+        } else {
+          atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
+          mbar_arrive(bars + s * 8);
+        }
+      }
+      ++issued;
+    };
+    while (issued < min(nk, kNs)) issue();
+
+    // ---- Q as the B operand of S^T -----------------------------------------
+    // Thread (r, t) holds, of query row r of each n-tile, channels 8 t .. 8 t + 7
+    // of every group: pairs (0,1), (2,3) for the group's first 16-deep product,
+    // (4,5), (6,7) for the second; the pairs that meet nibbles 1 and 3 of a
+    // word (codes * 2^-20) are scaled by 2^-4.
+    uint32_t qb[NT][kG][4];
+    float qsum[NT][2][kG];   // sum of q over the group (times 2^-24), columns 2t, 2t+1
+    float c_row[NT][2];      // score = c_row * (products), in log2 units
+    int lim[NT][2];          // visible keys of the row
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + r;
+      const int tok = row / p.group, hq = h * p.group + (row - tok * p.group);
+      const bool live = tok < n;
+      uint4 w[kG];
+      float big = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        w[g] = make_uint4(0, 0, 0, 0);
+        if (live)
+          w[g] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                  p.sq.row(b, hq, tok) + g * 32 + t * 8);
+        float x[8];
+        unpack2<kF16>(w[g].x, x[0], x[1]);
+        unpack2<kF16>(w[g].y, x[2], x[3]);
+        unpack2<kF16>(w[g].z, x[4], x[5]);
+        unpack2<kF16>(w[g].w, x[6], x[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          big = fmaxf(big, fabsf(x[i]));
+          finite = finite && fabsf(x[i]) < INFINITY;
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      finite = __shfl_xor_sync(0xffffffffu, (int)finite, 1) && finite;
+      finite = __shfl_xor_sync(0xffffffffu, (int)finite, 2) && finite;
+      // 2^(e - 127) <= big < 2^(e - 126), e its exponent field: q * up is below 2^11
+      const int e = max((int)(__float_as_uint(big) >> 23), 40);
+      const float up = big > 0.f && finite ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
+      // a row with an infinity or a NaN has no finite scores: they become NaN
+      const float back = !finite      ? __uint_as_float(0x7fffffffu)
+                         : big > 0.f ? __uint_as_float((uint32_t)(e - 10) << 23)
+                                     : 1.f;
+      float sum[kG];
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        const uint32_t in[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+        sum[g] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float a, c;
+          unpack2<kF16>(in[x], a, c);
+          a = finite ? a * up : 0.f;
+          c = finite ? c * up : 0.f;
+          sum[g] += a + c;
+          const float f4 = (x & 1) ? 0x1p-4f : 1.f;
+          qb[nt][g][x] = pack_f16x2(a * f4, c * f4);
+        }
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int src = (2 * t + y) * 4;
+#pragma unroll
+        for (int g = 0; g < kG; ++g)
+          qsum[nt][y][g] = __shfl_sync(0xffffffffu, sum[g], src) * 0x1p-24f;
+        c_row[nt][y] = __shfl_sync(0xffffffffu, back, src) * p.scale_log2 * 0x1p24f;
+        const int tk = (row0 + nt * 8 + 2 * t + y) / p.group;
+        lim[nt][y] = p.causal && tk < n ? len - n + tk + 1 : len;
+      }
+    }
+    // keys before `all` are visible to every row (rows behind the last new
+    // token see what they like and are written as zeros)
+    const int all = p.causal ? min(vis, len - n + row0 / p.group + 1) : vis;
+
+    float acc[kG][2][NT][4];  // O^T: channels 32 g + 4 r + 2 half + {0 (c0, c1), 1 (c2, c3)}
+    float acc_lo[NT][2][kG];  // sum of p lo over this thread's tokens
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        m[nt][y] = kNoMax;
+        l[nt][y] = 0.f;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          acc_lo[nt][y][g] = 0.f;
+          acc[g][0][nt][2 * y] = acc[g][0][nt][2 * y + 1] = 0.f;
+          acc[g][1][nt][2 * y] = acc[g][1][nt][2 * y + 1] = 0.f;
+        }
+      }
+
+    // One cell, in shared memory at `cell`. kMasked: some of its keys are
+    // hidden from some row, or its page was not found.
+    auto step = [&](uint32_t cell, int c, bool page_found, auto masked_tag) {
+      constexpr bool kMasked = decltype(masked_tag)::value;
+      // S^T: rows = slots r, r + 8; columns = query rows 2t, 2t + 1
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[nt][x] = 0.f;
+#pragma unroll
+      for (int sb = 0; sb < (kG + 3) / 4; ++sb) {
+        constexpr int kW = kG < 4 ? kG : 4;
+        uint32_t wa[kW], wb[kW], ga[kW], gb[kW];
+        lds_words<kW>(cell + k_word<D>(r, t, 4 * sb), wa);
+        lds_words<kW>(cell + k_word<D>(r + 8, t, 4 * sb), wb);
+        lds_words<kW>(cell + k_group<D>(r, 4 * sb), ga);
+        lds_words<kW>(cell + k_group<D>(r + 8, 4 * sb), gb);
+#pragma unroll
+        for (int x = 0; x < kW; ++x) {
+          const int g = 4 * sb + x;
+          float sa, la, sb8, lb;
+          unpack2<kF16>(ga[x], sa, la);
+          unpack2<kF16>(gb[x], sb8, lb);
+          const uint32_t wa8 = wa[x] >> 8, wb8 = wb[x] >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(d, wa[x] & 0x000f000fu, wb[x] & 0x000f000fu, wa[x] & 0x00f000f0u,
+                     wb[x] & 0x00f000f0u, qb[nt][g][0], qb[nt][g][1]);
+            mma16816(d, wa8 & 0x000f000fu, wb8 & 0x000f000fu, wa8 & 0x00f000f0u,
+                     wb8 & 0x00f000f0u, qb[nt][g][2], qb[nt][g][3]);
+            sc[nt][0] = fmaf(sa, d[0], fmaf(la, qsum[nt][0][g], sc[nt][0]));
+            sc[nt][1] = fmaf(sa, d[1], fmaf(la, qsum[nt][1][g], sc[nt][1]));
+            sc[nt][2] = fmaf(sb8, d[2], fmaf(lb, qsum[nt][0][g], sc[nt][2]));
+            sc[nt][3] = fmaf(sb8, d[3], fmaf(lb, qsum[nt][1][g], sc[nt][3]));
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[nt][x] *= c_row[nt][x & 1];
+
+      // V's groups of slots r, r + 8
+      uint32_t va[kG], vb[kG];
+      lds_words<kG>(cell + v_group<D>(r, 0), va);
+      lds_words<kG>(cell + v_group<D>(r + 8, 0), vb);
+      if constexpr (kMasked) {
+        const int ka = c * kCellTokens + cell_token(r), kb = ka + 8;
+        // rows behind the sequence may hold anything: s = lo = 0 keeps it out
+        const int end = page_found ? vis : 0;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          va[g] = ka < end ? va[g] : 0u;
+          vb[g] = kb < end ? vb[g] : 0u;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if ((x < 2 ? ka : kb) >= min(end, lim[nt][x & 1])) sc[nt][x] = -INFINITY;
+      }
+      float sa_max = kMinStep, sb_max = kMinStep;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        float s, lo;
+        unpack2<kF16>(va[g], s, lo);
+        sa_max = fmaxf(sa_max, s);
+        unpack2<kF16>(vb[g], s, lo);
+        sb_max = fmaxf(sb_max, s);
+      }
+      sa_max = fminf(sa_max, kMaxStep);
+      sb_max = fminf(sb_max, kMaxStep);
+
+      float pr[NT][4];
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          pr[nt][x] = ex2_approx(sc[nt][x] - m[nt][x & 1]);
+          over = over || pr[nt][x] * (x < 2 ? sa_max : sb_max) > 256.f;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+        const float la = lg2_approx(sa_max), lb = lg2_approx(sb_max);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float top = fmaxf(sc[nt][y] + la, sc[nt][2 + y] + lb);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float m_new = fmaxf(m[nt][y], top);
+            const float corr = ex2_approx(m[nt][y] - m_new);
+            m[nt][y] = m_new;
+            l[nt][y] *= corr;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              acc_lo[nt][y][g] *= corr;
+              acc[g][0][nt][y] *= corr;
+              acc[g][0][nt][2 + y] *= corr;
+              acc[g][1][nt][y] *= corr;
+              acc[g][1][nt][2 + y] *= corr;
+            }
+            pr[nt][y] = ex2_approx(sc[nt][y] - m_new);
+            pr[nt][2 + y] = ex2_approx(sc[nt][2 + y] - m_new);
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] += pr[nt][0] + pr[nt][2];
+        l[nt][1] += pr[nt][1] + pr[nt][3];
+      }
+
+      // V codes of slots 2t, 2t+1 (x = 0, 1) and 2t+8, 2t+9 (x = 2, 3)
+      constexpr int kPairs = kG / 2;
+      uint32_t vw[4][kPairs];
+      uint32_t vh[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int tok = t + 4 * x;  // cell_token(2t), (2t+1), (2t+8), (2t+9)
+        const uint32_t at = cell + v_piece<D>(tok, r);
+        if constexpr (kPairs == 1)
+          vw[x][0] = lds32(at);
+        else
+          lds_words<kPairs>(at, vw[x]);
+        if constexpr (kG & 1) vh[x] = lds16(cell + v_half<D>(tok, r, kG - 1));
+      }
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        float s0, lo0, s8, lo8;
+        unpack2<kF16>(va[g], s0, lo0);
+        unpack2<kF16>(vb[g], s8, lo8);
+        uint32_t xa, xb;
+        if ((kG & 1) && g == kG - 1) {
+          xa = vh[0] | (vh[1] << 16);
+          xb = vh[2] | (vh[3] << 16);
+        } else {
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          xa = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+          xb = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+        }
+        const uint32_t xa8 = xa >> 8, xb8 = xb >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          // a hidden key's p is 0, but its s may be infinite or NaN
+          auto mul = [](float pv, float s) { return kMasked && pv == 0.f ? 0.f : pv * s; };
+          const uint32_t b0 = transpose8x8(pack_f16x2(mul(pr[nt][0], s0), mul(pr[nt][1], s0)));
+          const uint32_t b1 = transpose8x8(pack_f16x2(mul(pr[nt][2], s8), mul(pr[nt][3], s8)));
+          acc_lo[nt][0][g] += mul(pr[nt][0], lo0) + mul(pr[nt][2], lo8);
+          acc_lo[nt][1][g] += mul(pr[nt][1], lo0) + mul(pr[nt][3], lo8);
+          mma16816(acc[g][0][nt], xa & 0x000f000fu, xa & 0x00f000f0u, xb & 0x000f000fu,
+                   xb & 0x00f000f0u, b0, b1);
+          mma16816(acc[g][1][nt], xa8 & 0x000f000fu, xa8 & 0x00f000f0u, xb8 & 0x000f000fu,
+                   xb8 & 0x00f000f0u, b0, b1);
+        }
+      }
+    };
+
+    // ---- the cells -----------------------------------------------------------
+    int done = 0;
+    for (; done < nk; ++done) {
+      const uint32_t stage = (fills + done) % kNs;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + stage * 8, ((fills + done) / kNs) & 1, st,
+                                             status_code(kKernCacheFwd, 1, 1))))
+        break;
+      const int c = c0 + kWarps * done;
+      const bool page_found = ok_flag[stage];
+      if (c * kCellTokens + kCellTokens > all || !page_found)
+        step(ring + stage * cell_bytes(D), c, page_found, std::true_type{});
+      else
+        step(ring + stage * cell_bytes(D), c, true, std::false_type{});
+      __syncwarp();  // every lane has read the stage
+      if (issued < nk) issue();
+    }
+    if (done < nk && !(p.debug_flags & kDebugSkipLoads))  // gave up: copies in flight still land
+      for (int k = done; k < issued; ++k)
+        mbar_wait_drain(bars + ((fills + k) % kNs) * 8, ((fills + k) / kNs) & 1, st,
+                        status_code(kKernCacheFwd, 1, 2));
+    fills += nk;
+
+    // ---- merge of the four warps ---------------------------------------------
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[nt][y] += __shfl_xor_sync(0xffffffffu, l[nt][y], o);
+#pragma unroll
+          for (int g = 0; g < kG; ++g)
+            acc_lo[nt][y][g] += __shfl_xor_sync(0xffffffffu, acc_lo[nt][y][g], o);
+        }
+    __syncwarp();
+    float *const out = reinterpret_cast<float *>(smem + warp * L::kWarp);  // [8 NT][kOutPitch]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = nt * 8 + 2 * t + y;
+        if (r == 0) {
+          stat[warp * kRows + row] = m[nt][y];
+          stat[(kWarps + warp) * kRows + row] = l[nt][y];
+        }
+#pragma unroll
+        for (int g = 0; g < kG; ++g)
+          *reinterpret_cast<float4 *>(out + row * L::kOutPitch + g * 32 + r * 4) = make_float4(
+              fmaf(acc[g][0][nt][y], 0x1p24f, acc_lo[nt][y][g]),
+              fmaf(acc[g][0][nt][2 + y], 0x1p20f, acc_lo[nt][y][g]),
+              fmaf(acc[g][1][nt][y], 0x1p24f, acc_lo[nt][y][g]),
+              fmaf(acc[g][1][nt][2 + y], 0x1p20f, acc_lo[nt][y][g]));
+      }
+    __syncthreads();
+    if (*(volatile int *)misc) {  // a wait gave up: nothing of this piece is written
+      if (threadIdx.x == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 1);
+      return;
+    }
+
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int slot = first_piece ? 0 : 1;
+    constexpr int kChunks = D / 4;  // 4 columns a thread
+    for (int x = threadIdx.x; x < kRows * kChunks; x += kThreads) {
+      const int row = x / kChunks, col = (x - row * kChunks) * 4;
+      float mm = kNoMax, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * kRows + row]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float wt = ex2_approx(stat[w * kRows + row] - mm);
+        const float4 a = *reinterpret_cast<const float4 *>(smem + w * L::kWarp +
+                                                           (row * L::kOutPitch + col) * 4);
+        ll = fmaf(wt, stat[(kWarps + w) * kRows + row], ll);
+        o.x = fmaf(wt, a.x, o.x);
+        o.y = fmaf(wt, a.y, o.y);
+        o.z = fmaf(wt, a.z, o.z);
+        o.w = fmaf(wt, a.w, o.w);
+      }
+      const int tok = (row0 + row) / p.group, hq = h * p.group + (row0 + row - tok * p.group);
+      const bool none = ll == 0.f || tok >= n;  // sees no key, or is no token
+      const float inv = 1.f / ll;
+      o = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const float lse2 = none ? -INFINITY : mm + lg2_approx(ll);
+      if (!whole) {
+        const size_t prow = ((size_t)blockIdx.x * 2 + slot) * kRows + row;
+        *reinterpret_cast<float4 *>(p.part + prow * D + col) = o;
+        if (col == 0) p.part_lse[prow] = lse2;
+      } else if (tok < p.nq) {
+        const size_t at = p.so.row(b, hq, tok) + col;
+        if (p.o_f32)
+          *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = o;
+        else
+          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
+              make_uint2(pack2<kF16>(o.x, o.y), pack2<kF16>(o.z, o.w));
+        if (col == 0) p.lse[((size_t)b * p.hq + hq) * p.nq + tok] = lse2 * kLn2;
+      }
+    }
+    // chain: the segment that begins here and ends in a later CTA (x: block,
+    // y: head, z: its slot here), and w: whether the segment that an earlier
+    // CTA began and that continues here ends here (1) or goes on (0)
+    if (t0 == 0 && t1 < tiles) chain = make_int4(blk, h, slot, chain.w);
+    if (first_piece && t0 > 0) chain.w = t1 == tiles;
+    first_piece = false;
+
+    f = seg_at + t1;
+    if (t1 == tiles && h == heads - 1) {
+      if (blk + 1 == n_blocks) break;
+      if (threadIdx.x == 0) {
+        int n2, len2, vis2;
+        blocks.shape(blk + 1, n2, len2, vis2, false);
+        misc[8] = blk + 1;
+        misc[9] = n2;
+        misc[10] = len2;
+        misc[11] = vis2;
+        *reinterpret_cast<long long *>(misc + 12) = f;
+      }
+    }
+    fence_proxy_async_smem();  // the next piece's copies overwrite the merge's reads and writes
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.chain[blockIdx.x] = chain;
+}
+
+// Merge of the parts of the segments that more than one CTA worked on: CTA x
+// merges the segment that begins in attention CTA x, if there is one, part by
+// part in the order of the axis:
+//     LSE = log sum_s 2^LSE_s,  O = sum_s 2^(LSE_s - LSE) O_s.
+template <int D, int NT, bool kF16>
+__global__ void __launch_bounds__(128)
+    fa_cache_combine_kernel(const __grid_constant__ CacheFwdParams p) {
+  constexpr int kRows = 8 * NT;
+  const int x = blockIdx.x;
+  const int4 c = p.chain[x];
+  if (c.x < 0) return;
+  int last = x + 1;
+  while (last < p.ctas - 1 && p.chain[last].w == 0) ++last;
+  const int row_blocks = (p.nq * p.group + kRows - 1) / kRows;
+  const int b = c.x / row_blocks, row0 = (c.x - b * row_blocks) * kRows;
+  auto part_row = [&](int s, int row) {
+    return ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
+  };
+  constexpr int kChunks = D / 4;
+  for (int y = threadIdx.x; y < kRows * kChunks; y += 128) {
+    const int row = y / kChunks, col = (y - row * kChunks) * 4;
+    const int tok = (row0 + row) / p.group, hq = c.y * p.group + (row0 + row - tok * p.group);
+    if (tok >= p.nq) continue;
+    float top = -INFINITY;
+    for (int s = x; s <= last; ++s) top = fmaxf(top, p.part_lse[part_row(s, row)]);
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = x; s <= last; ++s) {
+      const float lse2 = p.part_lse[part_row(s, row)];
+      if (lse2 == -INFINITY) continue;  // (a NaN goes on)
+      const float w = ex2_approx(lse2 - top);
+      const float4 a = *reinterpret_cast<const float4 *>(p.part + part_row(s, row) * D + col);
+      sum += w;
+      o.x = fmaf(w, a.x, o.x);
+      o.y = fmaf(w, a.y, o.y);
+      o.z = fmaf(w, a.z, o.z);
+      o.w = fmaf(w, a.w, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t at = p.so.row(b, hq, tok) + col;
+    if (p.o_f32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
+          make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
+    if (col == 0)
+      p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
+          sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
+  }
+}
+
+template <int D, int NT, bool kF16>
+cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
+  static std::atomic<bool> configured[64];  // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fa_cache_fwd_kernel<D, NT, kF16>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, NT>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev].store(true, std::memory_order_release);
+  }
+  {
+    LaunchProbe probe(kKindCacheFwd, stream);
+    fa_cache_fwd_kernel<D, NT, kF16><<<p.ctas, kThreads, Layout<D, NT>::kBytes, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  LaunchProbe probe(kKindCacheCombine, stream);
+  fa_cache_combine_kernel<D, NT, kF16><<<p.ctas, 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_t(const CacheFwdParams &p, cudaStream_t stream) {
+  return p.pool.f16 ? launch_d<D, NT, true>(p, stream) : launch_d<D, NT, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream) {
+  const bool two = cache_forward_row_tiles(p.pool.d, (long long)p.nq * p.group) == 2;
+  switch (p.pool.d) {
+    case 64: return two ? launch_t<64, 2>(p, stream) : launch_t<64, 1>(p, stream);
+    case 96: return two ? launch_t<96, 2>(p, stream) : launch_t<96, 1>(p, stream);
+    case 128: return two ? launch_t<128, 2>(p, stream) : launch_t<128, 1>(p, stream);
+    case 256: return launch_t<256, 1>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fa

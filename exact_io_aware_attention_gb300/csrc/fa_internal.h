@@ -132,7 +132,8 @@ struct BwdParams {
 enum KernelKind : int { kKindFwd = 0, kKindBwdPre = 1, kKindBwdDkdv = 2, kKindBwdDq = 3,
                         kKindFwdCombine = 4, kKindBwd256Dv = 5, kKindBwd256Dk = 6,
                         kKindBwd256Dq = 7, kKindBwdFused = 8, kKindBwdConvert = 9,
-                        kNumKinds = 10 };
+                        kKindCacheWrite = 10, kKindCacheRead = 11, kKindCacheFwd = 12,
+                        kKindCacheCombine = 13, kNumKinds = 14 };
 
 // Brackets one launch with CUDA events when measurement is enabled
 // (fa_profile_enable); a no-op otherwise.
@@ -177,9 +178,15 @@ cudaError_t launch_backward_d256(const BwdParams &p, cudaStream_t stream);
 // Status word codes: 0x80000000 | kernel << 16 | role << 8 | site.
 enum KernelId : uint32_t { kKernFwd = 1, kKernBwdPre = 2, kKernBwd = 3, kKernBwdDq = 4,
                            kKernBwd256Dv = 5, kKernBwd256Dk = 6, kKernBwd256Dq = 7,
-                           kKernBwdFused = 8 };
+                           kKernBwdFused = 8, kKernCacheWrite = 9, kKernCacheRead = 10,
+                           kKernCacheFwd = 11 };
 __host__ __device__ constexpr uint32_t status_code(uint32_t kernel, uint32_t role, uint32_t site) {
   return 0x80000000u | (kernel << 16) | (role << 8) | site;
+}
+// A value read on the device (a page, a position, a count) out of its range.
+constexpr uint32_t kIndexBit = 0x40000000u;
+__host__ __device__ constexpr uint32_t index_code(uint32_t kernel, uint32_t site) {
+  return kIndexBit | status_code(kernel, 0, site);
 }
 
 }  // namespace fa

@@ -98,7 +98,9 @@ typedef enum fa_status {
   FA_ERR_UNSUPPORTED = 2, /* valid but outside the supported set (d, N, dtype, stride) */
   FA_ERR_MISALIGNED = 3,  /* a pointer or a stride is not a multiple of 16 bytes */
   FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call or launch failed */
-  FA_ERR_TIMEOUT = 5      /* a kernel-side wait gave up (device status word) */
+  FA_ERR_TIMEOUT = 5,     /* a kernel-side wait gave up (device status word) */
+  FA_ERR_BAD_INDEX = 6    /* a page, position, length or count that a kernel read was out of
+                             range (device status word) */
 } fa_status;
 
 /* Version of this ABI; bumped on any incompatible change. */
@@ -291,12 +293,108 @@ fa_status fa_backward_noalloc(const void *Q, const void *K, const void *V, const
 /* Size in bytes of fa_backward_noalloc's fixed scratch area. */
 size_t fa_backward_noalloc_max_bytes(void);
 
+/* ---- Paged K/V cache in 4 bits ---------------------------------------------
+ *
+ * A cache is a pool of pages of page_size tokens each, for `heads` key/value
+ * heads of dimension d. A page table, an int32 device array of B rows of
+ * max_pages entries (row stride table_stride elements), says in which pages
+ * the tokens of each of B sequences lie: token p of sequence b is token
+ * p % page_size of page table[b][p / page_size]. Pages may be in any order
+ * and shared between sequences that only read them.
+ *
+ * Stored values. A row (one token, one head, K or V; 16-bit, of the cache's
+ * dtype) is cut into groups of 32 channels. Group x is stored as
+ *     lo = min x,   s = rn16((max x - lo) / 15),   u = min(15, rn((x - lo) / s))
+ * (u = 0 where s = 0) with 4-bit u and 16-bit lo and s, 5 bits a channel in
+ * all, and stands for lo + s u. Division is fp32, rounding to nearest even,
+ * rn16 to the cache's dtype. A group with a NaN or an infinity, or one whose
+ * range overflows s, stands for NaN. The arrangement of the bytes is the
+ * library's own (fa_cache_bytes gives their number): a cache is written and
+ * read by these calls only. A pool needs no initial contents.
+ *
+ * Device-side integers (page table, start, lengths, counts) are read by the
+ * kernels, so a captured graph follows their values from replay to replay.
+ * The host cannot check them: a page outside the pool, a token outside the
+ * table, a negative or too large length or count is not followed: such
+ * tokens are not written, read as zeros, and hidden from attention; lengths
+ * and counts are clamped; and the first one is recorded for
+ * fa_device_status() (FA_ERR_BAD_INDEX).
+ */
+
+/* A cache pool. `data`: device memory of fa_cache_bytes bytes, 16-byte
+ * aligned; page_size a multiple of 16; d in {64, 96, 128, 256}; dtype FA_BF16
+ * or FA_F16: the type of the K and V rows and of Q. `reserved` must be 0. */
+typedef struct fa_cache {
+  void *data;
+  int32_t num_pages, heads, page_size, d;
+  int32_t dtype;
+  int32_t reserved;
+} fa_cache;
+
+/* Bytes of a pool: num_pages * heads * page_size * (5/4) d; 0 for sizes outside
+ * the rules of fa_cache. */
+size_t fa_cache_bytes(int num_pages, int heads, int page_size, int d);
+
+/*
+ * Quantises K and V rows into the cache as they are written: row i of
+ * sequence b, i < counts[b] (all N without counts), becomes token
+ * start[b] + i. K, V: [B][heads][N][d], the cache's dtype, strides as for
+ * fa_tensor. start, counts: int32 device arrays [B]; counts may be NULL. Two
+ * sequences must not write the same token of the same page in one call. Other
+ * tokens stay as they were. A table row covers at most 2^24 tokens, and
+ * B * heads * N <= 2^31 - 1 (FA_ERR_UNSUPPORTED beyond).
+ */
+fa_status fa_cache_write(const fa_cache *cache, const fa_tensor *K, const fa_tensor *V,
+                         const int32_t *page_table, int64_t table_stride, int max_pages,
+                         const int32_t *start, const int32_t *counts, int B, int N,
+                         void *stream);
+
+/*
+ * Reads rows back: row i of sequence b of K and V (outputs, as above) is what
+ * token start[b] + i stands for, rounded once to the cache's dtype, for
+ * i < counts[b]; rows from counts[b] on are zeros.
+ */
+fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tensor *V,
+                        const int32_t *page_table, int64_t table_stride, int max_pages,
+                        const int32_t *start, const int32_t *counts, int B, int N,
+                        void *stream);
+
+/*
+ * Attention over the cache: O = softmax(scale Q K^T) V and LSE, where K and V
+ * are what the first lengths[b] tokens of sequence b stand for. Q, O:
+ * [B][Hq][Nq][d] of the cache's dtype (O also FA_F32); query head h reads
+ * cached head h / (Hq / heads), Hq a multiple of heads. LSE: fp32 contiguous
+ * [B][Hq][Nq]. lengths, counts: int32 device arrays [B]; counts may be NULL
+ * (all Nq). Query row i of sequence b, i < counts[b], is its token
+ * lengths[b] - counts[b] + i (the new tokens, already written, are the last
+ * ones); with causal it sees tokens up to itself, else all lengths[b]. A row
+ * that sees no token, and rows from counts[b] on, get O = 0 and LSE = -inf.
+ * B * Hq * Nq <= 2^30 - 1.
+ *
+ * The workspace (fa_cache_forward_workspace_bytes, 256-byte aligned) holds
+ * partial results while the call runs; calls that may overlap on the GPU need
+ * one each. Results do not depend on timing: equal calls on equal GPUs give
+ * equal bits.
+ */
+fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,
+                           int64_t table_stride, int max_pages, const int32_t *lengths,
+                           const int32_t *counts, const fa_tensor *O, float *LSE, int B, int Hq,
+                           int Nq, int causal, float scale, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of fa_cache_forward for Hq query heads over Hk cached heads
+ * and Nq query rows on the calling thread's current device (whatever the
+ * batch and the lengths; 0 for invalid sizes or without a device). */
+size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d);
+
 /*
  * Debug/status query: synchronises `stream`, reads the device status word
- * that kernel-side bounded waits set when they give up, clears it, and
- * stores it in *code (0 = no failure; otherwise an encoded kernel/role/wait
- * site). Returns FA_ERR_TIMEOUT if a wait gave up, FA_ERR_CUDA if the stream
- * reports an error, else FA_OK.
+ * that kernel-side bounded waits set when they give up and the cache kernels
+ * set when they skip an index out of range, clears it, and stores it in *code
+ * (0 = no failure; otherwise an encoded kernel/role/wait site, of the first
+ * failure since the last query). Returns FA_ERR_TIMEOUT if a wait gave up,
+ * FA_ERR_BAD_INDEX for an index, FA_ERR_CUDA if the stream reports an error,
+ * else FA_OK.
  */
 fa_status fa_device_status(void *stream, unsigned int *code);
 
@@ -318,7 +416,8 @@ fa_status fa_debug_configure(unsigned int flags, unsigned long long wait_limit_n
  * 0 forward, 1 backward preprocess (D_i and LSE*log2 e), 2 backward dK/dV,
  * 3 backward dQ, 4 merge of a split forward, for head dimension 256 the
  * backward's 5 dV, 6 dK and 7 dQ kernels, 8 the one-pass backward and 9 its
- * dQ conversion; fa_kernel_name() names them ("" for an unknown id).
+ * dQ conversion, 10 cache write, 11 cache read, 12 attention over a cache and
+ * 13 the merge of its parts; fa_kernel_name() names them ("" for an unknown id).
  *
  * fa_profile_enable(1): from then on every kernel launch is bracketed by two
  * CUDA events recorded on its stream (no synchronisation, no device memory).
