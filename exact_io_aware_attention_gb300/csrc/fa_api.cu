@@ -539,6 +539,12 @@ fa_status cache_pool(const fa_cache *c, const int32_t *table, int64_t table_stri
              c->page_size, kMaxCacheTokens);
     return FA_ERR_UNSUPPORTED;
   }
+  // cells are numbered in 32 bits
+  if ((double)c->num_pages * c->heads * (c->page_size / fa::kCellTokens) >= 4294967295.0) {
+    snprintf(g_last_error, sizeof(g_last_error), "cache: %d pages of %d tokens for %d heads",
+             c->num_pages, c->page_size, c->heads);
+    return FA_ERR_UNSUPPORTED;
+  }
   if (!aligned16(c->data) || !aligned4(table)) {
     snprintf(g_last_error, sizeof(g_last_error),
              "cache: data %p is not 16-byte aligned or page table %p not 4-byte aligned", c->data,

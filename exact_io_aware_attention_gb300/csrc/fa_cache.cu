@@ -6,7 +6,7 @@
 // and stands for lo + s u_c. lo is an element of the row, so it is exact in
 // the row's 16-bit type; s is rounded to it, which moves the largest element
 // by at most 15 s 2^-9 (bf16), a thirtieth of a step. A group with a
-// non-finite element, or whose range overflows, is stored as NaN.
+// non-finite element, or whose range overflows, is stored as s = 0, lo = NaN.
 //
 // Both kernels move each byte once: a thread owns 8 channels (16 bytes of a
 // row), four threads a group, and K and V of a row go together so that two
@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4 w, uint32_t (&u)[8]) {
     const float q = flat ? 0.f : fminf(rintf(__fdiv_rn(x[i] - lo, s)), 15.f);
     u[i] = (uint32_t)(int)q;
   }
-  return bad ? 0x7fff7fffu : (s16 | (round16<kF16>(lo) << 16));
+  return bad ? 0x7fff0000u : (s16 | (round16<kF16>(lo) << 16));
 }
 
 template <int D, bool kF16>

@@ -19,19 +19,24 @@
 // expanded in.
 //
 // Numbers. Q is scaled per row by a power of two and converted to f16
-// (exactly, down to 2^-24 of the row's largest element). P s is rounded to
-// f16 (2^-11 relative); so that it neither overflows nor underflows whatever
-// the size of V, the running reference m of the softmax follows
-// max_j (score_j + log2 s_j) and not the maximum score. Sums, m, l and the lo
-// terms are fp32. m moves only when p s would pass 2^8 (the result does not
-// depend on m), so that a cell costs a vote and no reduction.
+// (exactly, down to 2^-24 of the row's largest element). The sums of q over
+// the groups meet lo in one more product, each split into two or three 16-bit
+// terms (2^-17 relative or better). P s is rounded to f16 (2^-11 relative) to
+// P~; what the codes lose to that rounding is kept small by measuring them from
+// their middle:
+//     o_c = sum_j P~_jg u_jc - 7.5 sum_j P~_jg + sum_j p_j (lo_jg + 7.5 s_jg),
+// the middle sum from the tensor cores too. So that P~ neither overflows nor
+// underflows whatever the size of V, the running reference m of the softmax
+// follows max_j (score_j + log2 |v_j|) and not the maximum score. Sums, m, l
+// and the lo terms are fp32. m moves only when p s would pass 2^8 (the result
+// does not depend on m), so that a pair of cells costs a vote, no reduction.
 //
 // Work. The cells of a (query block, K/V head) are one segment; all segments
-// lie end to end on one axis, in units of four cells, and every CTA takes an
+// lie end to end on one axis, in units of eight cells, and every CTA takes an
 // equal share of it, whatever the lengths. A CTA's four warps take every
-// fourth cell, each with its own ring of bulk copies and its own m, l and O,
-// merged when the CTA leaves the segment. A segment within one CTA's share is
-// written out at once; parts of a segment go to scratch and
+// fourth pair of cells, each with its own ring of bulk copies and its own m, l
+// and O, merged when the CTA leaves the segment. A segment within one CTA's
+// share is written out at once; parts of a segment go to scratch and
 // fa_cache_combine_kernel merges them in the order of the axis: the results
 // do not depend on timing.
 #include <cuda_bf16.h>
@@ -48,28 +53,34 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kUnitTokens = 2 * kWarps * kCellTokens;  // a pair of cells for each warp
 constexpr int kMinShare = 2;       // units of a CTA at least
-constexpr float kNoMax = -1e30f;   // m before the first visible key
-constexpr float kMinStep = 0x1p-24f, kMaxStep = 0x1p100f;  // s as m sees it
+constexpr float kNoMax = -3e38f;   // m before the first visible key
+constexpr float kMid = 7.5f;       // the middle of the codes
 constexpr float kLn2 = 0.69314718055994531f;
+// m keeps p s below kMaxWeight, and p below kMaxWeight / kSmallStep unless V
+// is as small as that; |v| counts from 2^-90 (p and its sum stay finite).
+constexpr float kMaxWeight = 256.f, kSmallStep = 0x1p-32f;
+constexpr float kMinSize = 0x1p-90f, kMaxSize = 0x1p100f;
 
-// Ring of a warp: cells in flight. About 50 KB a CTA, 150-200 KB an SM: the
-// bytes in flight that HBM's latency needs.
-template <int D>
-constexpr int kStages = D == 256 ? 4 : D == 128 ? 5 : D == 96 ? 7 : 10;
+// Ring of a warp: pairs of cells in flight, what the SM's shared memory holds
+// for its CTAs: 150-200 KB an SM, the bytes in flight that HBM's latency needs.
+template <int D, int NT>
+constexpr int kStages = (220 * 1024 / cache_forward_ctas_per_sm(D, NT) - 2048) /
+                        (kWarps * 2 * cell_bytes(D));
 
 template <int D, int NT>
 struct Layout {
-  static constexpr int kRing = kStages<D> * cell_bytes(D);
+  static constexpr int kNs = kStages<D, NT>;
+  static constexpr int kRing = kNs * 2 * cell_bytes(D);
   static constexpr int kOutPitch = D + 4;  // floats: rows 4 banks apart
   static constexpr int kOut = 8 * NT * kOutPitch * 4;  // a warp's outputs reuse its ring
   static constexpr int kWarp = ((kRing > kOut ? kRing : kOut) + 127) / 128 * 128;
-  static constexpr int kBars = kWarps * kWarp;                      // [warp][stage] mbarriers
-  static constexpr int kOk = kBars + kWarps * kStages<D> * 8;        // [warp][stage] page found
-  static constexpr int kStat = kOk + kWarps * kStages<D> * 4;        // [warp][8 NT] m, then l
+  static constexpr int kBars = kWarps * kWarp;                       // [warp][stage] mbarriers
+  static constexpr int kStat = kBars + (kWarps * kNs * 8 + 15) / 16 * 16;  // [warp][8 NT] m, then l
   static constexpr int kMisc = kStat + 2 * kWarps * 8 * NT * 4;      // scan and flags
   static constexpr int kBytes = kMisc + 128;
-  static_assert(kBars % 8 == 0 && kMisc % 16 == 0, "alignment");
+  static_assert(kNs >= 2 && kBars % 8 == 0 && kMisc % 16 == 0, "ring and alignment");
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -79,6 +90,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same product of the cache's own type.
+template <bool kF16>
+__device__ __forceinline__ void mma16816_own(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kF16)
+    mma16816(d, a0, a1, a2, a3, b0, b1);
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Transpose of an 8x8 matrix of 16-bit elements spread over the warp.
@@ -147,7 +172,7 @@ struct Blocks {
   }
   // A segment without visible keys has one unit too: its rows are written.
   __device__ __forceinline__ int tiles(int vis) const {
-    return max(1, (vis + kWarps * kCellTokens - 1) / (kWarps * kCellTokens));
+    return max(1, (vis + kUnitTokens - 1) / kUnitTokens);
   }
 };
 
@@ -155,20 +180,22 @@ template <int D, int NT, bool kF16>
 __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     fa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using L = Layout<D, NT>;
-  constexpr int kG = D / 32, kNs = kStages<D>, kRows = 8 * NT;
+  constexpr int kG = D / 32, kNs = L::kNs, kRows = 8 * NT;
+  constexpr uint32_t kPairBytes = 2 * cell_bytes(D);
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, t = lane & 3;
   const uint32_t ring = sbase + warp * L::kWarp;
   const uint32_t bars = sbase + L::kBars + warp * kNs * 8;
-  volatile int *const ok_flag = reinterpret_cast<int *>(smem + L::kOk) + warp * kNs;
   float *const stat = reinterpret_cast<float *>(smem + L::kStat);
   // [0] abort, [4..7] scan, [8..13] the block of the next piece: number, new
   // tokens, length, visible keys, begin (64 bits)
   int *const misc = reinterpret_cast<int *>(smem + L::kMisc);
   const StatusSlot st = {p.status, misc, p.wait_limit_ns};
 
+  // the merge kernel may be set up meanwhile; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0)
     for (int s = 0; s < kNs; ++s) mbar_init(bars + s * 8, 1);
   if (threadIdx.x == 0) misc[0] = 0;
@@ -178,60 +205,69 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
   const int n_blocks = p.B * blocks.row_blocks, heads = p.pool.heads;
 
   // This CTA's share [f, f_end) of the axis: the total, then the block in
-  // which f lies, by block-wide scans over the blocks' sizes. Everything that
-  // decides which piece comes next is read once and handed to all threads
-  // through shared memory: they agree even on values that change under the
-  // kernel.
-  long long total = 0;
-  for (int x0 = 0; x0 < n_blocks; x0 += kThreads) {
-    const int x = x0 + threadIdx.x;
-    int n, len, vis, size = 0;
-    if (x < n_blocks) {
-      blocks.shape(x, n, len, vis, blockIdx.x == 0);
-      size = blocks.tiles(vis);
-    }
-    size = __reduce_add_sync(0xffffffffu, size);
-    if (lane == 0) misc[4 + warp] = size;
-    __syncthreads();
-    total += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
-    __syncthreads();
-  }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
-  long long f = share * blockIdx.x;
-  const long long f_end = min(f + share, total);
-  int4 chain = make_int4(-1, 0, 0, 0);
+  // which f lies, by block-wide scans over the blocks' sizes (one scan where
+  // the threads hold all blocks). Everything that decides which piece comes
+  // next is read once and handed to all threads through shared memory: they
+  // agree even on values that change under the kernel.
+  long long total = 0, share, f, f_end;
   bool found = false;
-  for (long long x0 = 0, at0 = 0; x0 < n_blocks && f < f_end && !found; x0 += kThreads) {
-    const int x = int(x0) + threadIdx.x;
-    int n = 0, len = 0, vis = 0, size = 0;
-    if (x < n_blocks) {
-      blocks.shape(x, n, len, vis, false);
-      size = blocks.tiles(vis);
-    }
-    int incl = size;
+  {
+    int x = threadIdx.x, n = 0, len = 0, vis = 0, size = 0;
+    long long at = 0;  // where block x begins
+    auto scan = [&](int x0, bool note) {
+      x = x0 + threadIdx.x;
+      size = 0;
+      if (x < n_blocks) {
+        blocks.shape(x, n, len, vis, note);
+        size = blocks.tiles(vis);
+      }
+      int incl = size;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) misc[4 + warp] = incl;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += misc[4 + w];
+      at = total + (long long)(before + incl - size) * heads;
+      total += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
+    };
+    auto find = [&] {
+      if (size > 0 && f >= at && f < at + (long long)size * heads) {
+        misc[8] = x;
+        misc[9] = n;
+        misc[10] = len;
+        misc[11] = vis;
+        *reinterpret_cast<long long *>(misc + 12) = at;
+      }
+      __syncthreads();
+    };
+    for (int x0 = 0; x0 < n_blocks; x0 += kThreads) {
+      if (x0 > 0) __syncthreads();  // misc[4..7] have been read
+      scan(x0, blockIdx.x == 0);
     }
-    if (lane == 31) misc[4 + warp] = incl;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += misc[4 + w];
-    const long long at = at0 + (long long)(before + incl - size) * heads;
-    if (size > 0 && f >= at && f < at + (long long)size * heads) {
-      misc[8] = x;
-      misc[9] = n;
-      misc[10] = len;
-      misc[11] = vis;
-      *reinterpret_cast<long long *>(misc + 12) = at;
+    share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
+    f = share * blockIdx.x;
+    f_end = min(f + share, total);
+    if (n_blocks <= kThreads) {
+      found = f < f_end;
+      find();
+    } else {
+      const long long all = total;
+      total = 0;
+      for (int x0 = 0; x0 < n_blocks && f < all && !found; x0 += kThreads) {
+        __syncthreads();
+        scan(x0, false);
+        find();
+        found = f < total;
+      }
     }
-    at0 += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
-    __syncthreads();
-    found = f < at0;
   }
+  int4 chain = make_int4(-1, 0, 0, 0);
 
-  uint32_t fills = 0;  // cells this warp has consumed over all pieces: ring position and parity
+  uint32_t stage = 0, phase = 0;  // ring position of the next pair to consume
   bool first_piece = true;
   while (found && f < f_end) {
     // ---- the piece: units [t0, t1) of a segment --------------------------
@@ -245,41 +281,64 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     const int t1 = int(min((long long)tiles, f_end - seg_at));
     const int b = blk / blocks.row_blocks, row0 = (blk - b * blocks.row_blocks) * kRows;
     const int cells = (vis + kCellTokens - 1) / kCellTokens;
-    // this warp's cells: c0 + 4 k, k < nk
-    const int c0 = t0 * kWarps + warp;
-    const int c_end = min(t1 * kWarps, cells);
-    const int nk = c0 < c_end ? (c_end - c0 + kWarps - 1) / kWarps : 0;
+    // this warp's pairs of cells: cells 2 (p0 + 4 k) and the next, k < nk
+    const int p0 = t0 * kWarps + warp;
+    const int p_end = min(t1 * kWarps, (cells + 1) / 2);
+    const int nk = p0 < p_end ? (p_end - p0 + kWarps - 1) / kWarps : 0;
 
-    // Page of cell k: lane k % 32 looks up the pages of 32 cells at a time,
-    // one batch ahead.
+    // Places of pair k's cells, as cell numbers of the pool: lane k % 32 looks
+    // up those of 32 pairs at a time, one batch ahead. A page holds an even
+    // number of cells, and the pair is one copy, or the two are found apart.
     const int32_t *const table = p.pool.table + (size_t)((long long)b * p.pool.table_stride);
-    auto page_of = [&](int k) {
-      return k < nk ? table[(c0 + kWarps * k) / p.pool.page_cells] : 0;
+    const bool apart = p.pool.page_cells & 1;
+    constexpr uint32_t kNoCell = 0xffffffffu;
+    bool bad_page = false;  // some page of this piece was not found
+    auto place = [&](int c) {
+      if (c >= cells) return kNoCell;
+      const int pi = c / p.pool.page_cells;
+      const int page = table[pi];
+      if (!p.pool.page_ok(page)) {
+        bad_page = true;
+        atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
+        return kNoCell;
+      }
+      return ((uint32_t)page * heads + h) * p.pool.page_cells + (c - pi * p.pool.page_cells);
     };
-    int pages = page_of(lane), pages_next = page_of(32 + lane);
+    uint32_t at0 = kNoCell, at1 = kNoCell, next0 = kNoCell, next1 = kNoCell;
+    auto look_up = [&](int k) {
+      next0 = next1 = kNoCell;
+      if (k + lane < nk) {
+        const int c = 2 * (p0 + kWarps * (k + lane));
+        next0 = place(c);
+        if (apart) next1 = place(c + 1);
+      }
+      bad_page = __any_sync(0xffffffffu, bad_page);
+    };
+    look_up(0);
+    at0 = next0;
+    at1 = next1;
+    if (nk > 32) look_up(32);
     int issued = 0;
+    uint32_t issue_stage = stage;
     auto issue = [&]() {
       const int k = issued;
       if ((k & 31) == 0 && k > 0) {
-        pages = pages_next;
-        pages_next = page_of(k + 32 + lane);
+        at0 = next0;
+        at1 = next1;
+        look_up(k + 32);
       }
-      const int page = __shfl_sync(0xffffffffu, pages, k & 31);
+      const uint32_t c0 = __shfl_sync(0xffffffffu, at0, k & 31);
+      const uint32_t c1 = apart ? __shfl_sync(0xffffffffu, at1, k & 31) : kNoCell;
       if (lane == 0 && !(p.debug_flags & kDebugSkipLoads)) {
-        const uint32_t s = (fills + k) % kNs;
-        const int c = c0 + kWarps * k;
-        const bool ok = p.pool.page_ok(page);
-        ok_flag[s] = ok;
-        if (ok) {
-          mbar_arrive_expect_tx(bars + s * 8, cell_bytes(D));
-          bulk_load_1d(ring + s * cell_bytes(D),
-                       p.pool.template cell_ptr<D>(page, h, c % p.pool.page_cells), cell_bytes(D),
-                       bars + s * 8);
-        } else {
-          atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
-          mbar_arrive(bars + s * 8);
-        }
+        const uint32_t bar = bars + issue_stage * 8, dst = ring + issue_stage * kPairBytes;
+        const uint32_t bytes0 = c0 == kNoCell ? 0u : apart ? kPairBytes / 2 : kPairBytes;
+        const uint32_t bytes1 = c1 == kNoCell ? 0u : kPairBytes / 2;
+        mbar_arrive_expect_tx(bar, bytes0 + bytes1);
+        if (bytes0) bulk_load_1d(dst, p.pool.data + (size_t)c0 * cell_bytes(D), bytes0, bar);
+        if (bytes1)
+          bulk_load_1d(dst + kPairBytes / 2, p.pool.data + (size_t)c1 * cell_bytes(D), bytes1, bar);
       }
+      if (++issue_stage == kNs) issue_stage = 0;
       ++issued;
     };
     while (issued < min(nk, kNs)) issue();
@@ -288,9 +347,13 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     // Thread (r, t) holds, of query row r of each n-tile, channels 8 t .. 8 t + 7
     // of every group: pairs (0,1), (2,3) for the group's first 16-deep product,
     // (4,5), (6,7) for the second; the pairs that meet nibbles 1 and 3 of a
-    // word (codes * 2^-20) are scaled by 2^-4.
+    // word (codes * 2^-20) are scaled by 2^-4. qs: the sums of q over the
+    // groups as the B operand of the product with lo, whose 16 columns are the
+    // groups (two, four or eight) repeated, with one term of a sum each.
+    constexpr int kGp = kG == 3 ? 4 : kG;
+    constexpr float kSumScale = kF16 ? 0x1p-6f : 0x1p-24f;  // f16 has no room for 2^-24
     uint32_t qb[NT][kG][4];
-    float qsum[NT][2][kG];   // sum of q over the group (times 2^-24), columns 2t, 2t+1
+    uint32_t qs[NT][2];
     float c_row[NT][2];      // score = c_row * (products), in log2 units
     int lim[NT][2];          // visible keys of the row
 #pragma unroll
@@ -325,15 +388,11 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       // 2^(e - 127) <= big < 2^(e - 126), e its exponent field: q * up is below 2^11
       const int e = max((int)(__float_as_uint(big) >> 23), 40);
       const float up = big > 0.f && finite ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
-      // a row with an infinity or a NaN has no finite scores: they become NaN
-      const float back = !finite      ? __uint_as_float(0x7fffffffu)
-                         : big > 0.f ? __uint_as_float((uint32_t)(e - 10) << 23)
-                                     : 1.f;
-      float sum[kG];
+      const float back = big > 0.f && finite ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f;
+      float sum[kGp] = {};
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         const uint32_t in[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
-        sum[g] = 0.f;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           float a, c;
@@ -346,14 +405,34 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         }
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+        // a row with an infinity or a NaN has no finite scores: they become NaN
+        sum[g] = finite ? sum[g] * kSumScale : __uint_as_float(0x7fffffffu);
+      }
+      // column k holds term k / kGp of group k % kGp; this thread's columns
+      // are 2 t, 2 t + 1 and the same plus 8
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const int k = half * 8 + 2 * tt;
+          float a = sum[k % kGp], c = sum[(k + 1) % kGp];
+          uint32_t pair = 0;
+#pragma unroll
+          for (int term = 0; term <= k / kGp; ++term) {
+            float ra, rc;
+            pair = term < 3 ? pack2<kF16>(a, c) : 0u;
+            unpack2<kF16>(pair, ra, rc);
+            a -= ra;
+            c -= rc;
+          }
+          word = tt == t ? pair : word;
+        }
+        qs[nt][half] = word;
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int src = (2 * t + y) * 4;
-#pragma unroll
-        for (int g = 0; g < kG; ++g)
-          qsum[nt][y][g] = __shfl_sync(0xffffffffu, sum[g], src) * 0x1p-24f;
-        c_row[nt][y] = __shfl_sync(0xffffffffu, back, src) * p.scale_log2 * 0x1p24f;
+        c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4) * p.scale_log2 * 0x1p24f;
         const int tk = (row0 + nt * 8 + 2 * t + y) / p.group;
         lim[nt][y] = p.causal && tk < n ? len - n + tk + 1 : len;
       }
@@ -363,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     const int all = p.causal ? min(vis, len - n + row0 / p.group + 1) : vis;
 
     float acc[kG][2][NT][4];  // O^T: channels 32 g + 4 r + 2 half + {0 (c0, c1), 1 (c2, c3)}
-    float acc_lo[NT][2][kG];  // sum of p lo over this thread's tokens
+    float acc_w[NT][4];       // row g: sum of P~ of group g (c0, c1 of the threads r = g)
+    float acc_lo[NT][2][kG];  // sum of p (lo + 7.5 s) over this thread's tokens
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -371,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       for (int y = 0; y < 2; ++y) {
         m[nt][y] = kNoMax;
         l[nt][y] = 0.f;
+        acc_w[nt][2 * y] = acc_w[nt][2 * y + 1] = 0.f;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
           acc_lo[nt][y][g] = 0.f;
@@ -379,97 +460,150 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         }
       }
 
-    // One cell, in shared memory at `cell`. kMasked: some of its keys are
-    // hidden from some row, or its page was not found.
-    auto step = [&](uint32_t cell, int c, bool page_found, auto masked_tag) {
+    // One pair of cells, in shared memory at `pair`, of which the first is
+    // cell c of the sequence. kMasked: some of its keys may be hidden from
+    // some row.
+    auto step = [&](uint32_t pair, int c, auto masked_tag) {
       constexpr bool kMasked = decltype(masked_tag)::value;
-      // S^T: rows = slots r, r + 8; columns = query rows 2t, 2t + 1
-      float sc[NT][4];
+      float sc[2][NT][4];              // products, then scores
+      uint32_t va[2][kG], vb[2][kG];   // V's groups of slots r, r + 8
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x2 = 0; x2 < 2; ++x2) {
+        const uint32_t cell = pair + x2 * cell_bytes(D);
+        // S^T: rows = slots r, r + 8; columns = query rows 2t, 2t + 1. First lo
+        // times the sums of q: columns 2t, 2t+1 (mod kGp) are two groups
+        uint32_t la, lb;
+        {
+          constexpr int kSteps = kGp / 2;  // threads t = 0 .. kSteps - 1 (mod) hold distinct groups
+          const int g0 = 2 * (t % kSteps);
+          uint32_t w0, w1, y0, y1;
+          if constexpr (kG == 3) {  // the fourth is no group; words are not paired
+            w0 = lds32(cell + k_group<D>(r, 0) + 4 * g0);
+            y0 = lds32(cell + k_group<D>(r + 8, 0) + 4 * g0);
+            w1 = g0 ? 0u : lds32(cell + k_group<D>(r, 1));
+            y1 = g0 ? 0u : lds32(cell + k_group<D>(r + 8, 1));
+          } else {
+            lds64(cell + k_group<D>(r, 0) + 4 * g0, w0, w1);
+            lds64(cell + k_group<D>(r + 8, 0) + 4 * g0, y0, y1);
+          }
+          la = __byte_perm(w0, w1, 0x7632);
+          lb = __byte_perm(y0, y1, 0x7632);
+        }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nt][x] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int sb = 0; sb < (kG + 3) / 4; ++sb) {
-        constexpr int kW = kG < 4 ? kG : 4;
-        uint32_t wa[kW], wb[kW], ga[kW], gb[kW];
-        lds_words<kW>(cell + k_word<D>(r, t, 4 * sb), wa);
-        lds_words<kW>(cell + k_word<D>(r + 8, t, 4 * sb), wb);
-        lds_words<kW>(cell + k_group<D>(r, 4 * sb), ga);
-        lds_words<kW>(cell + k_group<D>(r + 8, 4 * sb), gb);
+          for (int x = 0; x < 4; ++x) sc[x2][nt][x] = 0.f;
+          mma16816_own<kF16>(sc[x2][nt], la, lb, la, lb, qs[nt][0], qs[nt][1]);
+          if constexpr (kF16)
 #pragma unroll
-        for (int x = 0; x < kW; ++x) {
-          const int g = 4 * sb + x;
-          float sa, la, sb8, lb;
-          unpack2<kF16>(ga[x], sa, la);
-          unpack2<kF16>(gb[x], sb8, lb);
-          const uint32_t wa8 = wa[x] >> 8, wb8 = wb[x] >> 8;
+            for (int x = 0; x < 4; ++x) sc[x2][nt][x] *= 0x1p-18f;
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(d, wa[x] & 0x000f000fu, wb[x] & 0x000f000fu, wa[x] & 0x00f000f0u,
-                     wb[x] & 0x00f000f0u, qb[nt][g][0], qb[nt][g][1]);
-            mma16816(d, wa8 & 0x000f000fu, wb8 & 0x000f000fu, wa8 & 0x00f000f0u,
-                     wb8 & 0x00f000f0u, qb[nt][g][2], qb[nt][g][3]);
-            sc[nt][0] = fmaf(sa, d[0], fmaf(la, qsum[nt][0][g], sc[nt][0]));
-            sc[nt][1] = fmaf(sa, d[1], fmaf(la, qsum[nt][1][g], sc[nt][1]));
-            sc[nt][2] = fmaf(sb8, d[2], fmaf(lb, qsum[nt][0][g], sc[nt][2]));
-            sc[nt][3] = fmaf(sb8, d[3], fmaf(lb, qsum[nt][1][g], sc[nt][3]));
+        for (int sb = 0; sb < (kG + 3) / 4; ++sb) {
+          constexpr int kW = kG < 4 ? kG : 4;
+          uint32_t wa[kW], wb[kW], ga[kW], gb[kW];
+          lds_words<kW>(cell + k_word<D>(r, t, 4 * sb), wa);
+          lds_words<kW>(cell + k_word<D>(r + 8, t, 4 * sb), wb);
+          lds_words<kW>(cell + k_group<D>(r, 4 * sb), ga);
+          lds_words<kW>(cell + k_group<D>(r + 8, 4 * sb), gb);
+#pragma unroll
+          for (int x = 0; x < kW; ++x) {
+            const int g = 4 * sb + x;
+            float sa, sb8, unused;
+            unpack2<kF16>(ga[x], sa, unused);
+            unpack2<kF16>(gb[x], sb8, unused);
+            const uint32_t wa8 = wa[x] >> 8, wb8 = wb[x] >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816(d, wa[x] & 0x000f000fu, wb[x] & 0x000f000fu, wa[x] & 0x00f000f0u,
+                       wb[x] & 0x00f000f0u, qb[nt][g][0], qb[nt][g][1]);
+              mma16816(d, wa8 & 0x000f000fu, wb8 & 0x000f000fu, wa8 & 0x00f000f0u,
+                       wb8 & 0x00f000f0u, qb[nt][g][2], qb[nt][g][3]);
+              sc[x2][nt][0] = fmaf(sa, d[0], sc[x2][nt][0]);
+              sc[x2][nt][1] = fmaf(sa, d[1], sc[x2][nt][1]);
+              sc[x2][nt][2] = fmaf(sb8, d[2], sc[x2][nt][2]);
+              sc[x2][nt][3] = fmaf(sb8, d[3], sc[x2][nt][3]);
+            }
           }
         }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nt][x] *= c_row[nt][x & 1];
-
-      // V's groups of slots r, r + 8
-      uint32_t va[kG], vb[kG];
-      lds_words<kG>(cell + v_group<D>(r, 0), va);
-      lds_words<kG>(cell + v_group<D>(r + 8, 0), vb);
-      if constexpr (kMasked) {
-        const int ka = c * kCellTokens + cell_token(r), kb = ka + 8;
-        // rows behind the sequence may hold anything: s = lo = 0 keeps it out
-        const int end = page_found ? vis : 0;
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          va[g] = ka < end ? va[g] : 0u;
-          vb[g] = kb < end ? vb[g] : 0u;
-        }
+        // (rounded before m is taken off: with one rounding for both, a score
+        // beyond 2^24 could come out above the m that it set)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if ((x < 2 ? ka : kb) >= min(end, lim[nt][x & 1])) sc[nt][x] = -INFINITY;
-      }
-      float sa_max = kMinStep, sb_max = kMinStep;
+          for (int x = 0; x < 4; ++x) sc[x2][nt][x] = __fmul_rn(sc[x2][nt][x], c_row[nt][x & 1]);
+        lds_words<kG>(cell + v_group<D>(r, 0), va[x2]);
+        lds_words<kG>(cell + v_group<D>(r + 8, 0), vb[x2]);
+        if constexpr (kMasked) {
+          const int cc = c + x2;
+          const bool there =
+              cc < cells && !(bad_page && !p.pool.page_ok(table[cc / p.pool.page_cells]));
+          // rows behind the sequence may hold anything: s = lo = 0 keeps it out
+          const int end = there ? vis : 0;
+          const int ka = cc * kCellTokens + cell_token(r), kb = ka + 8;
 #pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        float s, lo;
-        unpack2<kF16>(va[g], s, lo);
-        sa_max = fmaxf(sa_max, s);
-        unpack2<kF16>(vb[g], s, lo);
-        sb_max = fmaxf(sb_max, s);
+          for (int g = 0; g < kG; ++g) {
+            va[x2][g] = ka < end ? va[x2][g] : 0u;
+            vb[x2][g] = kb < end ? vb[x2][g] : 0u;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if ((x < 2 ? ka : kb) >= min(end, lim[nt][x & 1]))
+                sc[x2][nt][x] = -INFINITY;
+        }
       }
-      sa_max = fminf(sa_max, kMaxStep);
-      sb_max = fminf(sb_max, kMaxStep);
 
-      float pr[NT][4];
+      float pr[2][NT][4];
       bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x2 = 0; x2 < 2; ++x2) {
+        float sa = kSmallStep, sb = kSmallStep;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          pr[nt][x] = ex2_approx(sc[nt][x] - m[nt][x & 1]);
-          over = over || pr[nt][x] * (x < 2 ? sa_max : sb_max) > 256.f;
+        for (int g = 0; g < kG; ++g) {
+          float s, lo;
+          unpack2<kF16>(va[x2][g], s, lo);
+          sa = fmaxf(sa, s);
+          unpack2<kF16>(vb[x2][g], s, lo);
+          sb = fmaxf(sb, s);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            pr[x2][nt][x] = ex2_approx(sc[x2][nt][x] - m[nt][x & 1]);
+          over = over || fmaxf(fmaxf(pr[x2][nt][0], pr[x2][nt][1]) * sa,
+                               fmaxf(pr[x2][nt][2], pr[x2][nt][3]) * sb) > kMaxWeight;
+        }
+      }
       if (__any_sync(0xffffffffu, over)) {
-        const float la = lg2_approx(sa_max), lb = lg2_approx(sb_max);
+        // the sizes of the tokens' values, in log2: steps, and lo as far as it
+        // stands out
+        float size[2][2];
+#pragma unroll
+        for (int x2 = 0; x2 < 2; ++x2) {
+          float sa = kMinSize, sb = kMinSize;
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            float s, lo;
+            unpack2<kF16>(va[x2][g], s, lo);
+            sa = fmaxf(sa, fmaxf(s, fabsf(lo) * 0x1p-10f));
+            unpack2<kF16>(vb[x2][g], s, lo);
+            sb = fmaxf(sb, fmaxf(s, fabsf(lo) * 0x1p-10f));
+          }
+          size[x2][0] = lg2_approx(fminf(sa, kMaxSize));
+          size[x2][1] = lg2_approx(fminf(sb, kMaxSize));
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float top = fmaxf(sc[nt][y] + la, sc[nt][2 + y] + lb);
+            float top = kNoMax;
+#pragma unroll
+            for (int x2 = 0; x2 < 2; ++x2)
+              top = fmaxf(top, fmaxf(sc[x2][nt][y] + size[x2][0], sc[x2][nt][2 + y] + size[x2][1]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -477,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
             const float corr = ex2_approx(m[nt][y] - m_new);
             m[nt][y] = m_new;
             l[nt][y] *= corr;
+            acc_w[nt][y] *= corr;
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               acc_lo[nt][y][g] *= corr;
@@ -485,82 +620,100 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
               acc[g][1][nt][y] *= corr;
               acc[g][1][nt][2 + y] *= corr;
             }
-            pr[nt][y] = ex2_approx(sc[nt][y] - m_new);
-            pr[nt][2 + y] = ex2_approx(sc[nt][2 + y] - m_new);
+#pragma unroll
+            for (int x2 = 0; x2 < 2; ++x2) {
+              pr[x2][nt][y] = ex2_approx(sc[x2][nt][y] - m_new);
+              pr[x2][nt][2 + y] = ex2_approx(sc[x2][nt][2 + y] - m_new);
+            }
           }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] += pr[nt][0] + pr[nt][2];
-        l[nt][1] += pr[nt][1] + pr[nt][3];
-      }
 
-      // V codes of slots 2t, 2t+1 (x = 0, 1) and 2t+8, 2t+9 (x = 2, 3)
-      constexpr int kPairs = kG / 2;
-      uint32_t vw[4][kPairs];
-      uint32_t vh[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int tok = t + 4 * x;  // cell_token(2t), (2t+1), (2t+8), (2t+9)
-        const uint32_t at = cell + v_piece<D>(tok, r);
-        if constexpr (kPairs == 1)
-          vw[x][0] = lds32(at);
-        else
-          lds_words<kPairs>(at, vw[x]);
-        if constexpr (kG & 1) vh[x] = lds16(cell + v_half<D>(tok, r, kG - 1));
-      }
-#pragma unroll
-      for (int g = 0; g < kG; ++g) {
-        float s0, lo0, s8, lo8;
-        unpack2<kF16>(va[g], s0, lo0);
-        unpack2<kF16>(vb[g], s8, lo8);
-        uint32_t xa, xb;
-        if ((kG & 1) && g == kG - 1) {
-          xa = vh[0] | (vh[1] << 16);
-          xb = vh[2] | (vh[3] << 16);
-        } else {
-          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-          xa = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-          xb = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-        }
-        const uint32_t xa8 = xa >> 8, xb8 = xb >> 8;
+      for (int x2 = 0; x2 < 2; ++x2) {
+        const uint32_t cell = pair + x2 * cell_bytes(D);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          // a hidden key's p is 0, but its s may be infinite or NaN
-          auto mul = [](float pv, float s) { return kMasked && pv == 0.f ? 0.f : pv * s; };
-          const uint32_t b0 = transpose8x8(pack_f16x2(mul(pr[nt][0], s0), mul(pr[nt][1], s0)));
-          const uint32_t b1 = transpose8x8(pack_f16x2(mul(pr[nt][2], s8), mul(pr[nt][3], s8)));
-          acc_lo[nt][0][g] += mul(pr[nt][0], lo0) + mul(pr[nt][2], lo8);
-          acc_lo[nt][1][g] += mul(pr[nt][1], lo0) + mul(pr[nt][3], lo8);
-          mma16816(acc[g][0][nt], xa & 0x000f000fu, xa & 0x00f000f0u, xb & 0x000f000fu,
-                   xb & 0x00f000f0u, b0, b1);
-          mma16816(acc[g][1][nt], xa8 & 0x000f000fu, xa8 & 0x00f000f0u, xb8 & 0x000f000fu,
-                   xb8 & 0x00f000f0u, b0, b1);
+          l[nt][0] += pr[x2][nt][0] + pr[x2][nt][2];
+          l[nt][1] += pr[x2][nt][1] + pr[x2][nt][3];
+        }
+        // V codes of slots 2t, 2t+1 (x = 0, 1) and 2t+8, 2t+9 (x = 2, 3)
+        constexpr int kPairs = kG / 2;
+        uint32_t vw[4][kPairs];
+        uint32_t vh[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int tok = t + 4 * x;  // cell_token(2t), (2t+1), (2t+8), (2t+9)
+          const uint32_t at = cell + v_piece<D>(tok, r);
+          if constexpr (kPairs == 1)
+            vw[x][0] = lds32(at);
+          else
+            lds_words<kPairs>(at, vw[x]);
+          if constexpr (kG & 1) vh[x] = lds16(cell + v_half<D>(tok, r, kG - 1));
+        }
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          float s0, lo0, s8, lo8;
+          unpack2<kF16>(va[x2][g], s0, lo0);
+          unpack2<kF16>(vb[x2][g], s8, lo8);
+          lo0 = fmaf(kMid, s0, lo0);
+          lo8 = fmaf(kMid, s8, lo8);
+          uint32_t xa, xb;
+          if ((kG & 1) && g == kG - 1) {
+            xa = vh[0] | (vh[1] << 16);
+            xb = vh[2] | (vh[3] << 16);
+          } else {
+            const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+            xa = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+            xb = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+          }
+          const uint32_t xa8 = xa >> 8, xb8 = xb >> 8;
+          const uint32_t ones = r == g ? 0x3c003c00u : 0u;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float *pv = pr[x2][nt];
+            const uint32_t b0 = transpose8x8(pack_f16x2(pv[0] * s0, pv[1] * s0));
+            const uint32_t b1 = transpose8x8(pack_f16x2(pv[2] * s8, pv[3] * s8));
+            // a hidden key's p is 0, but its lo may be NaN
+            auto mul = [](float a, float x) { return kMasked && a == 0.f ? 0.f : a * x; };
+            acc_lo[nt][0][g] += mul(pv[0], lo0) + mul(pv[2], lo8);
+            acc_lo[nt][1][g] += mul(pv[1], lo0) + mul(pv[3], lo8);
+            mma16816(acc[g][0][nt], xa & 0x000f000fu, xa & 0x00f000f0u, xb & 0x000f000fu,
+                     xb & 0x00f000f0u, b0, b1);
+            mma16816(acc[g][1][nt], xa8 & 0x000f000fu, xa8 & 0x00f000f0u, xb8 & 0x000f000fu,
+                     xb8 & 0x00f000f0u, b0, b1);
+            mma16816(acc_w[nt], ones, 0u, ones, 0u, b0, b1);
+          }
         }
       }
     };
 
-    // ---- the cells -----------------------------------------------------------
+    // ---- the pairs of cells ----------------------------------------------------
     int done = 0;
     for (; done < nk; ++done) {
-      const uint32_t stage = (fills + done) % kNs;
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + stage * 8, ((fills + done) / kNs) & 1, st,
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + stage * 8, phase, st,
                                              status_code(kKernCacheFwd, 1, 1))))
         break;
-      const int c = c0 + kWarps * done;
-      const bool page_found = ok_flag[stage];
-      if (c * kCellTokens + kCellTokens > all || !page_found)
-        step(ring + stage * cell_bytes(D), c, page_found, std::true_type{});
+      const int c = 2 * (p0 + kWarps * done);
+      if ((c + 2) * kCellTokens > all || bad_page)
+        step(ring + stage * kPairBytes, c, std::true_type{});
       else
-        step(ring + stage * cell_bytes(D), c, true, std::false_type{});
+        step(ring + stage * kPairBytes, c, std::false_type{});
       __syncwarp();  // every lane has read the stage
+      if (++stage == kNs) {
+        stage = 0;
+        phase ^= 1;
+      }
       if (issued < nk) issue();
     }
-    if (done < nk && !(p.debug_flags & kDebugSkipLoads))  // gave up: copies in flight still land
-      for (int k = done; k < issued; ++k)
-        mbar_wait_drain(bars + ((fills + k) % kNs) * 8, ((fills + k) / kNs) & 1, st,
-                        status_code(kKernCacheFwd, 1, 2));
-    fills += nk;
+    if (done < nk && !(p.debug_flags & kDebugSkipLoads)) {  // gave up: copies in flight still land
+      for (int k = done; k < issued; ++k) {
+        mbar_wait_drain(bars + stage * 8, phase, st, status_code(kKernCacheFwd, 1, 2));
+        if (++stage == kNs) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
 
     // ---- merge of the four warps ---------------------------------------------
 #pragma unroll
@@ -574,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           for (int g = 0; g < kG; ++g)
             acc_lo[nt][y][g] += __shfl_xor_sync(0xffffffffu, acc_lo[nt][y][g], o);
         }
-    __syncwarp();
     float *const out = reinterpret_cast<float *>(smem + warp * L::kWarp);  // [8 NT][kOutPitch]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -585,6 +737,9 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           stat[warp * kRows + row] = m[nt][y];
           stat[(kWarps + warp) * kRows + row] = l[nt][y];
         }
+#pragma unroll
+        for (int g = 0; g < kG; ++g)  // minus 7.5 times the sum of P~, which the threads r = g hold
+          acc_lo[nt][y][g] -= kMid * __shfl_sync(0xffffffffu, acc_w[nt][y], g * 4 + t);
 #pragma unroll
         for (int g = 0; g < kG; ++g)
           *reinterpret_cast<float4 *>(out + row * L::kOutPitch + g * 32 + r * 4) = make_float4(
@@ -665,56 +820,105 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
   if (threadIdx.x == 0) p.chain[blockIdx.x] = chain;
 }
 
-// Merge of the parts of the segments that more than one CTA worked on: CTA x
-// merges the segment that begins in attention CTA x, if there is one, part by
-// part in the order of the axis:
-//     LSE = log sum_s 2^LSE_s,  O = sum_s 2^(LSE_s - LSE) O_s.
+// Merge of the parts of the segments that more than one CTA worked on: block
+// (x, y) merges row y of the segment that begins in attention CTA x, if there
+// is one:  LSE = log sum_s 2^LSE_s,  O = sum_s 2^(LSE_s - LSE) O_s.
+// A thread holds 4 columns; kSub threads share a column's parts, each every
+// kSub-th, so that a chain over the whole GPU is a few loads deep.
+constexpr int kCombineThreads = 256;
+
 template <int D, int NT, bool kF16>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kCombineThreads)
     fa_cache_combine_kernel(const __grid_constant__ CacheFwdParams p) {
-  constexpr int kRows = 8 * NT;
-  const int x = blockIdx.x;
+  constexpr int kRows = 8 * NT, kChunks = D / 4, kSub = kCombineThreads / kChunks;
+  __shared__ float4 s_o[kSub][kChunks];
+  __shared__ float s_top[kSub], s_sum[kSub];
+  __shared__ int s_last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int x = blockIdx.x, row = blockIdx.y;
   const int4 c = p.chain[x];
   if (c.x < 0) return;
-  int last = x + 1;
-  while (last < p.ctas - 1 && p.chain[last].w == 0) ++last;
   const int row_blocks = (p.nq * p.group + kRows - 1) / kRows;
   const int b = c.x / row_blocks, row0 = (c.x - b * row_blocks) * kRows;
-  auto part_row = [&](int s, int row) {
-    return ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
-  };
-  constexpr int kChunks = D / 4;
-  for (int y = threadIdx.x; y < kRows * kChunks; y += 128) {
-    const int row = y / kChunks, col = (y - row * kChunks) * 4;
-    const int tok = (row0 + row) / p.group, hq = c.y * p.group + (row0 + row - tok * p.group);
-    if (tok >= p.nq) continue;
-    float top = -INFINITY;
-    for (int s = x; s <= last; ++s) top = fmaxf(top, p.part_lse[part_row(s, row)]);
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = x; s <= last; ++s) {
-      const float lse2 = p.part_lse[part_row(s, row)];
-      if (lse2 == -INFINITY) continue;  // (a NaN goes on)
-      const float w = ex2_approx(lse2 - top);
-      const float4 a = *reinterpret_cast<const float4 *>(p.part + part_row(s, row) * D + col);
-      sum += w;
-      o.x = fmaf(w, a.x, o.x);
-      o.y = fmaf(w, a.y, o.y);
-      o.z = fmaf(w, a.z, o.z);
-      o.w = fmaf(w, a.w, o.w);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t at = p.so.row(b, hq, tok) + col;
-    if (p.o_f32)
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    else
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
-          make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
-    if (col == 0)
-      p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
-          sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
+  const int tok = (row0 + row) / p.group, hq = c.y * p.group + (row0 + row - tok * p.group);
+  if (tok >= p.nq) return;
+  // the first later CTA in which the segment ends
+  if (threadIdx.x == 0) s_last = p.ctas - 1;
+  __syncthreads();
+  for (int s = x + 1; s < p.ctas; s += kCombineThreads) {
+    const int y = s + threadIdx.x;
+    if (y < p.ctas && p.chain[y].w != 0) atomicMin(&s_last, y);
+    __syncthreads();
+    if (s_last < s + kCombineThreads) break;
+    __syncthreads();
   }
+  const int last = s_last;
+  const int sub = threadIdx.x / kChunks, chunk = threadIdx.x - sub * kChunks;
+  if (sub < kSub) {
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;
+    for (int s0 = x + sub; s0 <= last; s0 += kBatch * kSub) {
+      float lse2[kBatch];
+      float4 a[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + i * kSub;
+        const size_t prow = ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
+        lse2[i] = s <= last ? p.part_lse[prow] : -INFINITY;
+        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s <= last) a[i] = *reinterpret_cast<const float4 *>(p.part + prow * D + chunk * 4);
+      }
+      float high = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) high = fmaxf(high, lse2[i]);
+      const float corr = top == -INFINITY ? 0.f : ex2_approx(top - high);
+      if (top != -INFINITY) {
+        sum *= corr;
+        o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
+      }
+      top = high;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // (a part without keys counts nothing; a NaN goes on)
+        const float w = lse2[i] == -INFINITY ? 0.f : ex2_approx(lse2[i] - top);
+        sum += w;
+        o = make_float4(fmaf(w, a[i].x, o.x), fmaf(w, a[i].y, o.y), fmaf(w, a[i].z, o.z),
+                        fmaf(w, a[i].w, o.w));
+      }
+    }
+    s_o[sub][chunk] = o;
+    if (chunk == 0) {
+      s_top[sub] = top;
+      s_sum[sub] = sum;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x >= kChunks) return;
+  float top = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kSub; ++i) top = fmaxf(top, s_top[i]);
+#pragma unroll
+  for (int i = 0; i < kSub; ++i) {
+    if (s_sum[i] == 0.f) continue;
+    // a NaN among a thread's parts leaves its top finite or at -inf and its sum NaN
+    const float w = s_top[i] == -INFINITY ? 1.f : ex2_approx(s_top[i] - top);
+    const float4 a = s_o[i][threadIdx.x];
+    sum = fmaf(w, s_sum[i], sum);
+    o = make_float4(fmaf(w, a.x, o.x), fmaf(w, a.y, o.y), fmaf(w, a.z, o.z), fmaf(w, a.w, o.w));
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const size_t at = p.so.row(b, hq, tok) + threadIdx.x * 4;
+  if (p.o_f32)
+    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
+        make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
+  if (threadIdx.x == 0)
+    p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
+        sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
 }
 
 template <int D, int NT, bool kF16>
@@ -735,13 +939,28 @@ cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
+  // set up while the attention kernel runs (programmatic dependent launch)
   LaunchProbe probe(kKindCacheCombine, stream);
-  fa_cache_combine_kernel<D, NT, kF16><<<p.ctas, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  const long long rows = (long long)p.nq * p.group;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < 8 * NT ? rows : 8 * NT));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_cache_combine_kernel<D, NT, kF16>, p);
 }
 
 template <int D, int NT>
-cudaError_t launch_t(const CacheFwdParams &p, cudaStream_t stream) {
+cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
+  // no more CTAs than units that sequences as long as the table could have
+  CacheFwdParams p = all;
+  const double units = (double)p.B * ((p.nq * p.group + 8 * NT - 1) / (8 * NT)) * p.pool.heads *
+                       ((p.pool.table_cells * kCellTokens + kUnitTokens - 1) / kUnitTokens);
+  if (units < (double)p.ctas * kMinShare) p.ctas = (int)(units + kMinShare - 1) / kMinShare;
   return p.pool.f16 ? launch_d<D, NT, true>(p, stream) : launch_d<D, NT, false>(p, stream);
 }
 

@@ -336,6 +336,15 @@ def test_non_finite_values_stay_where_they_are_seen(d):
         assert torch.equal(o, good_o) and torch.equal(lse, good_lse)
 
 
+def test_a_nan_query_that_sees_nothing():
+    c, table, q, k, v = attend_case(1, 2, 1, 3, [20], 64, 16, BF16, True)
+    q[0, 0] = float("nan")
+    o, lse = fa().cache_forward(q.cuda(), c, table.cuda(), ints([2]), causal=True)
+    clean()
+    assert (o[0, :, 0] == 0).all() and torch.isneginf(lse[0, :, 0]).all()
+    assert torch.isnan(o[0, 0, 1:]).all() and torch.isfinite(o[0, 1]).all()
+
+
 def test_zero_and_tiny_queries():
     d = 128
     c, table, q, k, v = attend_case(1, 8, 1, 1, [200], d, 64, BF16, False)
