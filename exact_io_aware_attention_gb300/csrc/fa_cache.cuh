@@ -148,6 +148,9 @@ constexpr int cache_forward_row_tiles(int d, long long rows) {
 }
 // CTAs of the attention kernel that one SM holds (its registers allow).
 constexpr int cache_forward_ctas_per_sm(int d, int row_tiles) {
+#ifdef FA_C128
+  if (row_tiles == 1 && d == 128) return FA_C128;
+#endif
   return row_tiles == 1 ? (d == 256 ? 2 : d == 128 ? 3 : 4) : (d == 64 ? 3 : 2);
 }
 

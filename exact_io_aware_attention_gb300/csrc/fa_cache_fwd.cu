@@ -63,6 +63,12 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kMaxWeight = 256.f, kSmallStep = 0x1p-32f;
 constexpr float kMinSize = 0x1p-90f, kMaxSize = 0x1p100f;
 
+// Cells of a pair that a warp works on together.
+#ifndef FA_KF
+#define FA_KF 1
+#endif
+constexpr int cells_at_once(int d, int row_tiles) { return FA_KF; }
+
 // Ring of a warp: pairs of cells in flight, what the SM's shared memory holds
 // for its CTAs: 150-200 KB an SM, the bytes in flight that HBM's latency needs.
 template <int D, int NT>
@@ -180,7 +186,7 @@ template <int D, int NT, bool kF16>
 __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     fa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using L = Layout<D, NT>;
-  constexpr int kG = D / 32, kNs = L::kNs, kRows = 8 * NT;
+  constexpr int kG = D / 32, kNs = L::kNs, kRows = 8 * NT, kF = cells_at_once(D, NT);
   constexpr uint32_t kPairBytes = 2 * cell_bytes(D);
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 
     float acc[kG][2][NT][4];  // O^T: channels 32 g + 4 r + 2 half + {0 (c0, c1), 1 (c2, c3)}
     float acc_w[NT][4];       // row g: sum of P~ of group g (c0, c1 of the threads r = g)
-    float acc_lo[NT][2][kG];  // sum of p (lo + 7.5 s) over this thread's tokens
+    uint64_t acc_lo[NT][2][kG];  // sums of p (lo + 7.5 s) over this thread's slots r, r + 8 (a pair)
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -454,22 +460,21 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         acc_w[nt][2 * y] = acc_w[nt][2 * y + 1] = 0.f;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          acc_lo[nt][y][g] = 0.f;
+          acc_lo[nt][y][g] = 0;  // (0.f, 0.f)
           acc[g][0][nt][2 * y] = acc[g][0][nt][2 * y + 1] = 0.f;
           acc[g][1][nt][2 * y] = acc[g][1][nt][2 * y + 1] = 0.f;
         }
       }
 
-    // One pair of cells, in shared memory at `pair`, of which the first is
-    // cell c of the sequence. kMasked: some of its keys may be hidden from
-    // some row.
-    auto step = [&](uint32_t pair, int c, auto masked_tag) {
+    // kF cells, in shared memory at `at`, of which the first is cell c of the
+    // sequence. kMasked: some of their keys may be hidden from some row.
+    auto step = [&](uint32_t at, int c, auto masked_tag) {
       constexpr bool kMasked = decltype(masked_tag)::value;
-      float sc[2][NT][4];              // products, then scores
-      uint32_t va[2][kG], vb[2][kG];   // V's groups of slots r, r + 8
+      float sc[kF][NT][4];              // products, then scores
+      uint32_t va[kF][kG], vb[kF][kG];  // V's groups of slots r, r + 8
 #pragma unroll
-      for (int x2 = 0; x2 < 2; ++x2) {
-        const uint32_t cell = pair + x2 * cell_bytes(D);
+      for (int x2 = 0; x2 < kF; ++x2) {
+        const uint32_t cell = at + x2 * cell_bytes(D);
         // S^T: rows = slots r, r + 8; columns = query rows 2t, 2t + 1. First lo
         // times the sums of q: columns 2t, 2t+1 (mod kGp) are two groups
         uint32_t la, lb;
@@ -532,7 +537,10 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sc[x2][nt][x] = __fmul_rn(sc[x2][nt][x], c_row[nt][x & 1]);
+          for (int x = 0; x < 4; x += 2)
+            f2unpack(fmul2(f2pack(sc[x2][nt][x], sc[x2][nt][x + 1]),
+                           f2pack(c_row[nt][0], c_row[nt][1])),
+                     sc[x2][nt][x], sc[x2][nt][x + 1]);
         lds_words<kG>(cell + v_group<D>(r, 0), va[x2]);
         lds_words<kG>(cell + v_group<D>(r + 8, 0), vb[x2]);
         if constexpr (kMasked) {
@@ -551,15 +559,29 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if ((x < 2 ? ka : kb) >= min(end, lim[nt][x & 1]))
-                sc[x2][nt][x] = -INFINITY;
+              if ((x < 2 ? ka : kb) >= min(end, lim[nt][x & 1])) sc[x2][nt][x] = -INFINITY;
         }
       }
 
-      float pr[2][NT][4];
+      float pr[kF][NT][4];
       bool over = false;
+      auto weights = [&] {
 #pragma unroll
-      for (int x2 = 0; x2 < 2; ++x2) {
+        for (int x2 = 0; x2 < kF; ++x2)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; x += 2) {
+              float a, b2;
+              f2unpack(fsub2(f2pack(sc[x2][nt][x], sc[x2][nt][x + 1]),
+                             f2pack(m[nt][0], m[nt][1])), a, b2);
+              pr[x2][nt][x] = ex2_approx(a);
+              pr[x2][nt][x + 1] = ex2_approx(b2);
+            }
+      };
+      weights();
+#pragma unroll
+      for (int x2 = 0; x2 < kF; ++x2) {
         float sa = kSmallStep, sb = kSmallStep;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
@@ -570,20 +592,16 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           sb = fmaxf(sb, s);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            pr[x2][nt][x] = ex2_approx(sc[x2][nt][x] - m[nt][x & 1]);
+        for (int nt = 0; nt < NT; ++nt)
           over = over || fmaxf(fmaxf(pr[x2][nt][0], pr[x2][nt][1]) * sa,
                                fmaxf(pr[x2][nt][2], pr[x2][nt][3]) * sb) > kMaxWeight;
-        }
       }
       if (__any_sync(0xffffffffu, over)) {
         // the sizes of the tokens' values, in log2: steps, and lo as far as it
         // stands out
-        float size[2][2];
+        float size[kF][2];
 #pragma unroll
-        for (int x2 = 0; x2 < 2; ++x2) {
+        for (int x2 = 0; x2 < kF; ++x2) {
           float sa = kMinSize, sb = kMinSize;
 #pragma unroll
           for (int g = 0; g < kG; ++g) {
@@ -602,40 +620,40 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           for (int y = 0; y < 2; ++y) {
             float top = kNoMax;
 #pragma unroll
-            for (int x2 = 0; x2 < 2; ++x2)
+            for (int x2 = 0; x2 < kF; ++x2)
               top = fmaxf(top, fmaxf(sc[x2][nt][y] + size[x2][0], sc[x2][nt][2 + y] + size[x2][1]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float m_new = fmaxf(m[nt][y], top);
             const float corr = ex2_approx(m[nt][y] - m_new);
+            const uint64_t corr2 = f2pack(corr, corr);
             m[nt][y] = m_new;
             l[nt][y] *= corr;
             acc_w[nt][y] *= corr;
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-              acc_lo[nt][y][g] *= corr;
+              acc_lo[nt][y][g] = fmul2(acc_lo[nt][y][g], corr2);
               acc[g][0][nt][y] *= corr;
               acc[g][0][nt][2 + y] *= corr;
               acc[g][1][nt][y] *= corr;
               acc[g][1][nt][2 + y] *= corr;
             }
-#pragma unroll
-            for (int x2 = 0; x2 < 2; ++x2) {
-              pr[x2][nt][y] = ex2_approx(sc[x2][nt][y] - m_new);
-              pr[x2][nt][2 + y] = ex2_approx(sc[x2][nt][2 + y] - m_new);
-            }
           }
+        weights();
       }
 
 #pragma unroll
-      for (int x2 = 0; x2 < 2; ++x2) {
-        const uint32_t cell = pair + x2 * cell_bytes(D);
+      for (int x2 = 0; x2 < kF; ++x2) {
+        const uint32_t cell = at + x2 * cell_bytes(D);
+        uint64_t p2[NT][2];  // the weights of slots r, r + 8 of query row 2t + y
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          l[nt][0] += pr[x2][nt][0] + pr[x2][nt][2];
-          l[nt][1] += pr[x2][nt][1] + pr[x2][nt][3];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            p2[nt][y] = f2pack(pr[x2][nt][y], pr[x2][nt][2 + y]);
+            l[nt][y] += pr[x2][nt][y] + pr[x2][nt][2 + y];
+          }
         // V codes of slots 2t, 2t+1 (x = 0, 1) and 2t+8, 2t+9 (x = 2, 3)
         constexpr int kPairs = kG / 2;
         uint32_t vw[4][kPairs];
@@ -643,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int tok = t + 4 * x;  // cell_token(2t), (2t+1), (2t+8), (2t+9)
-          const uint32_t at = cell + v_piece<D>(tok, r);
+          const uint32_t piece = cell + v_piece<D>(tok, r);
           if constexpr (kPairs == 1)
-            vw[x][0] = lds32(at);
+            vw[x][0] = lds32(piece);
           else
-            lds_words<kPairs>(at, vw[x]);
+            lds_words<kPairs>(piece, vw[x]);
           if constexpr (kG & 1) vh[x] = lds16(cell + v_half<D>(tok, r, kG - 1));
         }
 #pragma unroll
@@ -655,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           float s0, lo0, s8, lo8;
           unpack2<kF16>(va[x2][g], s0, lo0);
           unpack2<kF16>(vb[x2][g], s8, lo8);
-          lo0 = fmaf(kMid, s0, lo0);
-          lo8 = fmaf(kMid, s8, lo8);
+          const uint64_t s2 = f2pack(s0, s8);
+          const uint64_t mid2 = ffma2(f2pack(kMid, kMid), s2, f2pack(lo0, lo8));
           uint32_t xa, xb;
           if ((kG & 1) && g == kG - 1) {
             xa = vh[0] | (vh[1] << 16);
@@ -670,13 +688,26 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           const uint32_t ones = r == g ? 0x3c003c00u : 0u;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float *pv = pr[x2][nt];
-            const uint32_t b0 = transpose8x8(pack_f16x2(pv[0] * s0, pv[1] * s0));
-            const uint32_t b1 = transpose8x8(pack_f16x2(pv[2] * s8, pv[3] * s8));
-            // a hidden key's p is 0, but its lo may be NaN
-            auto mul = [](float a, float x) { return kMasked && a == 0.f ? 0.f : a * x; };
-            acc_lo[nt][0][g] += mul(pv[0], lo0) + mul(pv[2], lo8);
-            acc_lo[nt][1][g] += mul(pv[1], lo0) + mul(pv[3], lo8);
+            float w0, w8, y0, y8;
+            f2unpack(fmul2(p2[nt][0], s2), w0, w8);
+            f2unpack(fmul2(p2[nt][1], s2), y0, y8);
+            const uint32_t b0 = transpose8x8(pack_f16x2(w0, y0));
+            const uint32_t b1 = transpose8x8(pack_f16x2(w8, y8));
+            if constexpr (kMasked) {
+              // a hidden key's p is 0, but its lo may be NaN
+              float m0, m8;
+              f2unpack(mid2, m0, m8);
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                acc_lo[nt][y][g] =
+                    fadd2(acc_lo[nt][y][g],
+                          f2pack(pr[x2][nt][y] == 0.f ? 0.f : pr[x2][nt][y] * m0,
+                                 pr[x2][nt][2 + y] == 0.f ? 0.f : pr[x2][nt][2 + y] * m8));
+            } else {
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                acc_lo[nt][y][g] = ffma2(p2[nt][y], mid2, acc_lo[nt][y][g]);
+            }
             mma16816(acc[g][0][nt], xa & 0x000f000fu, xa & 0x00f000f0u, xb & 0x000f000fu,
                      xb & 0x00f000f0u, b0, b1);
             mma16816(acc[g][1][nt], xa8 & 0x000f000fu, xa8 & 0x00f000f0u, xb8 & 0x000f000fu,
@@ -694,10 +725,15 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
                                              status_code(kKernCacheFwd, 1, 1))))
         break;
       const int c = 2 * (p0 + kWarps * done);
-      if ((c + 2) * kCellTokens > all || bad_page)
-        step(ring + stage * kPairBytes, c, std::true_type{});
-      else
-        step(ring + stage * kPairBytes, c, std::false_type{});
+      const bool masked = (c + 2) * kCellTokens > all || bad_page;
+#pragma unroll 1
+      for (int x = 0; x < 2; x += kF) {
+        const uint32_t at = ring + stage * kPairBytes + x * cell_bytes(D);
+        if (masked)
+          step(at, c + x, std::true_type{});
+        else
+          step(at, c + x, std::false_type{});
+      }
       __syncwarp();  // every lane has read the stage
       if (++stage == kNs) {
         stage = 0;
@@ -723,9 +759,21 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           l[nt][y] += __shfl_xor_sync(0xffffffffu, l[nt][y], o);
+        }
+    float sum_lo[NT][2][kG];  // the sums over all slots, minus 7.5 times the sum of P~, which
+                              // the threads r = g hold
 #pragma unroll
-          for (int g = 0; g < kG; ++g)
-            acc_lo[nt][y][g] += __shfl_xor_sync(0xffffffffu, acc_lo[nt][y][g], o);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          float a, c;
+          f2unpack(acc_lo[nt][y][g], a, c);
+          a += c;
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+          sum_lo[nt][y][g] = a - kMid * __shfl_sync(0xffffffffu, acc_w[nt][y], g * 4 + t);
         }
     float *const out = reinterpret_cast<float *>(smem + warp * L::kWarp);  // [8 NT][kOutPitch]
 #pragma unroll
@@ -738,15 +786,12 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           stat[(kWarps + warp) * kRows + row] = l[nt][y];
         }
 #pragma unroll
-        for (int g = 0; g < kG; ++g)  // minus 7.5 times the sum of P~, which the threads r = g hold
-          acc_lo[nt][y][g] -= kMid * __shfl_sync(0xffffffffu, acc_w[nt][y], g * 4 + t);
-#pragma unroll
         for (int g = 0; g < kG; ++g)
           *reinterpret_cast<float4 *>(out + row * L::kOutPitch + g * 32 + r * 4) = make_float4(
-              fmaf(acc[g][0][nt][y], 0x1p24f, acc_lo[nt][y][g]),
-              fmaf(acc[g][0][nt][2 + y], 0x1p20f, acc_lo[nt][y][g]),
-              fmaf(acc[g][1][nt][y], 0x1p24f, acc_lo[nt][y][g]),
-              fmaf(acc[g][1][nt][2 + y], 0x1p20f, acc_lo[nt][y][g]));
+              fmaf(acc[g][0][nt][y], 0x1p24f, sum_lo[nt][y][g]),
+              fmaf(acc[g][0][nt][2 + y], 0x1p20f, sum_lo[nt][y][g]),
+              fmaf(acc[g][1][nt][y], 0x1p24f, sum_lo[nt][y][g]),
+              fmaf(acc[g][1][nt][2 + y], 0x1p20f, sum_lo[nt][y][g]));
       }
     __syncthreads();
     if (*(volatile int *)misc) {  // a wait gave up: nothing of this piece is written
