@@ -68,7 +68,7 @@ SIGNATURES = {
     "fa_cache_read": ([_cp, _tp, _tp, _vp, _i64, _i, _vp, _vp, _i, _i, _vp], _i),
     "fa_cache_forward": ([_tp, _cp, _vp, _i64, _i, _vp, _vp, _tp, _vp, _i, _i, _i, _i, _f, _vp,
                           _sz, _vp], _i),
-    "fa_cache_forward_workspace_bytes": ([_i, _i, _i, _i], _sz),
+    "fa_cache_forward_workspace_bytes": ([_i, _i, _i, _i, _i], _sz),
     "fa_device_status": ([_vp, ctypes.POINTER(ctypes.c_uint)], _i),
     "fa_debug_configure": ([ctypes.c_uint, ctypes.c_ulonglong], _i),
     "fa_num_kernels": ([], _i),
@@ -327,6 +327,7 @@ class KVCache4:
         self.num_pages, self.heads, self.d, self.page_size = num_pages, heads, d, page_size
         self.dtype = dtype
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self._ws_bytes = {}  # of cache_forward, by (Hq, Nq, pages a table row)
         self._desc = FaCache(self.data.data_ptr(), num_pages, heads, page_size, d,
                              _DTYPES[dtype], 0)
 
@@ -433,31 +434,29 @@ def cache_forward(q, cache: KVCache4, page_table, lengths, causal: bool = False,
     table, stride, pages = _table(page_table, B, dev)
     ln, cnt = _ints(lengths, B, "lengths", dev), _ints(counts, B, "counts", dev)
     if workspace is None:
-        workspace = torch.empty(cache_forward_workspace_bytes(Hq, cache.heads, Nq, d, dev),
-                                dtype=torch.uint8, device=dev)
+        nbytes = cache._ws_bytes.get((Hq, Nq, pages))
+        if nbytes is None:
+            nbytes = cache._ws_bytes[Hq, Nq, pages] = cache_forward_workspace_bytes(
+                Hq, cache.heads, Nq, d, pages * cache.page_size, dev)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous, on the cache's device {dev}")
     _check(_lib_fast().fa_cache_forward(
         _desc(q, "q"), cache._desc, table, stride, pages, ln, cnt, _desc(out, "out"),
-        lse.data_ptr(), B, Hq, Nq, int(bool(causal)), scale, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(dev)), "fa_cache_forward")
+        lse.data_ptr(), B, Hq, Nq, int(bool(causal)), scale,
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev)),
+        "fa_cache_forward")
     return out, lse
 
 
-_cache_ws = {}
-
-
-def cache_forward_workspace_bytes(Hq, Hk, Nq, d, device=None) -> int:
+def cache_forward_workspace_bytes(Hq, Hk, Nq, d, max_tokens, device=None) -> int:
     """Workspace bytes of ``cache_forward`` on ``device`` (default: the current CUDA
-    device), whatever the batch and the lengths."""
-    idx = torch.device(device).index if device is not None else None
-    idx = torch.cuda.current_device() if idx is None else idx
-    n = _cache_ws.get((idx, Hq, Hk, Nq, d))
-    if n is None:
-        with torch.cuda.device(idx):
-            n = int(_lib_fast().fa_cache_forward_workspace_bytes(Hq, Hk, Nq, d))
-        _cache_ws[(idx, Hq, Hk, Nq, d)] = n
-    return n
+    device) for page tables of ``max_tokens`` tokens a row, whatever the batch
+    and the lengths; 0 where it needs none."""
+    with torch.cuda.device(device):
+        return int(_lib_fast().fa_cache_forward_workspace_bytes(Hq, Hk, Nq, d, max_tokens))
 
 
 def device_status(stream=None) -> int:

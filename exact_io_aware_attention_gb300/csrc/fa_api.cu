@@ -602,7 +602,7 @@ struct CacheScratch {
   int ctas;
   size_t part, lse, chain;
 };
-bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, CacheScratch *out) {
+bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, long long tokens, CacheScratch *out) {
   if (sms <= 0 || Hk <= 0) return false;
   const int nt = fa::cache_forward_row_tiles(d, (long long)(Hq / Hk) * Nq);
   out->ctas = sms * fa::cache_forward_ctas_per_sm(d, nt);
@@ -610,6 +610,7 @@ bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, CacheScratch *out) {
   out->part = round_up(rows * d * sizeof(float));
   out->lse = round_up(rows * sizeof(float));
   out->chain = round_up((size_t)out->ctas * sizeof(int4));
+  if (fa::cache_forward_whole(tokens)) out->part = out->lse = out->chain = 0;
   return true;
 }
 
@@ -625,7 +626,9 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
   memset(&p, 0, sizeof(p));
   fa_status s = cache_pool(cache, table, table_stride, max_pages, B, &p.pool);
   if (s != FA_OK) return s;
-  if (!Q || !O || !LSE || !lengths || !workspace) return FA_ERR_INVALID_ARG;
+  const long long tokens = (long long)max_pages * cache->page_size;
+  p.whole = fa::cache_forward_whole(tokens) ? 1 : 0;
+  if (!Q || !O || !LSE || !lengths || (!workspace && !p.whole)) return FA_ERR_INVALID_ARG;
   if (Hq % cache->heads != 0) {
     snprintf(g_last_error, sizeof(g_last_error), "%d query heads over %d cached heads", Hq,
              cache->heads);
@@ -644,7 +647,7 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
     return FA_ERR_MISALIGNED;
   if ((s = bind_device(cache->data)) != FA_OK) return s;
   CacheScratch w;
-  if (!cache_scratch(sm_count(), Hq, cache->heads, Nq, d, &w))
+  if (!cache_scratch(sm_count(), Hq, cache->heads, Nq, d, tokens, &w))
     return cuda_fail("SM count", cudaErrorInvalidDevice);
   if (ws_bytes < w.part + w.lse + w.chain) {
     snprintf(g_last_error, sizeof(g_last_error), "workspace of %zu bytes, %zu needed", ws_bytes,
@@ -959,10 +962,10 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
                          false, stream);
 }
 
-size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d) {
-  if (Hq < 0 || Hk <= 0 || Nq < 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
+size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d, int max_tokens) {
+  if (Hq < 0 || Hk <= 0 || Nq < 0 || max_tokens < 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
   CacheScratch w;
-  return cache_scratch(sm_count(), Hq, Hk, Nq, d, &w) ? w.part + w.lse + w.chain : 0;
+  return cache_scratch(sm_count(), Hq, Hk, Nq, d, max_tokens, &w) ? w.part + w.lse + w.chain : 0;
 }
 
 fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,

@@ -133,19 +133,9 @@ __global__ void __launch_bounds__(kRowsPerBlock *(D / 8))
     v1 |= uv[4 + x] << (4 * x);  // halfword r = 2t + 1
   }
   const int slot = cell_slot(at.token);
-  if constexpr (D == 96) {
-    if (!at.cell) return;
-    *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t, g)) = (uint16_t)v0;
-    *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t + 1, g)) = (uint16_t)v1;
-  } else {
-    // groups come in pairs of a word: the even group's quad stores the word
-    // of r = 2t, the odd group's the word of r = 2t + 1
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, (g & 1) ? v0 : v1, 4);
-    const uint32_t word = (g & 1) ? (other | (v1 << 16)) : (v0 | (other << 16));
-    if (!at.cell) return;
-    *reinterpret_cast<uint32_t *>(at.cell + v_piece<D>(at.token, 2 * t + (g & 1)) +
-                                  (g >> 1) * 4) = word;
-  }
+  if (!at.cell) return;
+  *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t, g)) = (uint16_t)v0;
+  *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t + 1, g)) = (uint16_t)v1;
   *reinterpret_cast<uint32_t *>(at.cell + k_word<D>(slot, t, g)) = kw;
   if (t == 0) *reinterpret_cast<uint32_t *>(at.cell + k_group<D>(slot, g)) = gk;
   if (t == 1) *reinterpret_cast<uint32_t *>(at.cell + v_group<D>(slot, g)) = gv;

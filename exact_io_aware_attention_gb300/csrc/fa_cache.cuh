@@ -6,7 +6,7 @@
 // copy brings a cell, or a run of cells of a page, into shared memory:
 //
 //   offset 0      K codes   16 rows of d/2 bytes
-//          8 d    V codes   16 rows of d/2 bytes
+//          8 d    V codes   8 rows of d bytes, for pairs of tokens
 //          16 d   K groups  16 rows of d/32 words: s (low half), lo (high half)
 //          18 d   V groups  likewise
 //
@@ -17,11 +17,11 @@
 // the subnormal u * 2^-24 (u * 2^-20 one nibble up), exact in the product.
 //
 //   token j of a cell is matrix row cell_slot(j); K codes and both group
-//   arrays are in slot order, V codes in token order;
+//   arrays are in slot order;
 //   K: channel c = 32 g + 8 t + i is nibble i/2 of the (i%2)-th half of word
 //   (t, g): the halves are the two k-neighbours of the product;
-//   V: channel c = 32 g + 4 r + i is nibble i of halfword (r, g): the
-//   k-neighbours are two tokens, paired up by a byte permute when read.
+//   V: channel c = 32 g + 4 r + i of tokens t + 8 y and t + 8 y + 4, which are
+//   k-neighbours, is nibble i of the halves of word (y, t, r, g).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -56,21 +56,21 @@ __host__ __device__ constexpr int k_word(int slot, int t, int g) {
                   : slot * (D / 2) + (t * (D / 32) + g) * 4;
 }
 
-// Byte offset of the first V word that thread row r reads of token j, and of
-// halfword (j, r, g): 4 channels of one group. Groups are paired in words
-// (two words a thread for d = 128, four for d = 256; the last group of d = 96
-// follows as halfwords); the order of the threads' pieces depends on the
-// token so that four consecutive tokens lie in different banks.
+// Byte offset of V's code word (y, t, r, g): 4 channels of tokens t + 8 y and
+// t + 8 y + 4. Thread row r's words of a pair lie together (d = 256: four and
+// four); their order depends on t so that the four threads t of a load lie in
+// different banks (d = 96: they do as it is).
 template <int D>
-__host__ __device__ constexpr int v_piece(int j, int r) {
-  return cell_v_codes(D) + j * (D / 2) +
-         (D == 256   ? (r ^ ((j & 3) << 1)) * 16
-          : D == 128 ? (r ^ ((j & 2) << 1)) * 8
-                     : r * 4);
+__host__ __device__ constexpr int v_word(int y, int t, int r, int g) {
+  return cell_v_codes(D) +
+         (D == 256   ? (g >> 2) * 1024 + (4 * y + t) * 128 + (r ^ (2 * t)) * 16 + (g & 3) * 4
+          : D == 128 ? (4 * y + t) * 128 + (r ^ (2 * t)) * 16 + g * 4
+          : D == 96  ? (4 * y + t) * 96 + (r * 3 + g) * 4
+                     : (4 * y + t) * 64 + (r ^ (4 * (t >> 1))) * 8 + g * 4);
 }
 template <int D>
 __host__ __device__ constexpr int v_half(int j, int r, int g) {
-  return D == 96 && g == 2 ? cell_v_codes(D) + j * (D / 2) + 32 + r * 2 : v_piece<D>(j, r) + g * 2;
+  return v_word<D>(j >> 3, j & 3, r, g) + ((j >> 2) & 1) * 2;
 }
 
 // Byte offset of the group word (s, lo) of a slot.
@@ -129,6 +129,7 @@ struct CacheFwdParams {
   float *part;                        // scratch: [ctas][2][rows][d] partial outputs,
   float *part_lse;                    // [ctas][2][rows] their log2-sum-exp,
   int4 *chain;                        // [ctas] where a segment's parts lie
+  int whole;                          // no segment is split: no scratch, no merge
   int ctas;                           // CTAs of the attention kernel
   unsigned int *status;
   uint32_t debug_flags;
@@ -146,6 +147,11 @@ cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream);
 constexpr int cache_forward_row_tiles(int d, long long rows) {
   return d == 256 || rows <= 8 ? 1 : 2;
 }
+// Whether sequences of at most `tokens` tokens are not split between CTAs.
+#ifndef FA_WHOLE
+#define FA_WHOLE 1024
+#endif
+constexpr bool cache_forward_whole(long long tokens) { return tokens <= FA_WHOLE; }
 // CTAs of the attention kernel that one SM holds (its registers allow).
 constexpr int cache_forward_ctas_per_sm(int d, int row_tiles) {
 #ifdef FA_C128

@@ -33,7 +33,9 @@
 //
 // Work. The cells of a (query block, K/V head) are one segment; all segments
 // lie end to end on one axis, in units of eight cells, and every CTA takes an
-// equal share of it, whatever the lengths. A CTA's four warps take every
+// equal share of it, whatever the lengths. (Where the page table holds so few
+// tokens that a merge would cost more than it saves, segments stay whole.)
+// A CTA's four warps take every
 // fourth pair of cells, each with its own ring of bulk copies and its own m, l
 // and O, merged when the CTA leaves the segment. A segment within one CTA's
 // share is written out at once; parts of a segment go to scratch and
@@ -64,9 +66,16 @@ constexpr float kMaxWeight = 256.f, kSmallStep = 0x1p-32f;
 constexpr float kMinSize = 0x1p-90f, kMaxSize = 0x1p100f;
 
 // Cells of a pair that a warp works on together.
+#ifndef FA_VE
+#define FA_VE 0
+#endif
+#ifndef FA_UX
+#define FA_UX 1
+#endif
 #ifndef FA_KF
 #define FA_KF 1
 #endif
+constexpr int kUX = FA_UX;
 constexpr int cells_at_once(int d, int row_tiles) { return FA_KF; }
 
 // Ring of a warp: pairs of cells in flight, what the SM's shared memory holds
@@ -134,12 +143,6 @@ __device__ __forceinline__ void lds128(uint32_t a, uint32_t &x, uint32_t &y, uin
                : "r"(a)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
-
 // kN consecutive words; the address is aligned to the widest load that fits.
 template <int kN>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *w) {
@@ -176,6 +179,9 @@ struct Blocks {
     const int last = min((rb * rows + rows - 1) / p.group, n - 1);
     vis = first >= n ? 0 : p.causal ? min(len, max(len - n + last + 1, 0)) : len;
   }
+  // Its segments' weight on the work axis: their units, or one for a segment
+  // that stays whole.
+  __device__ __forceinline__ int weight(int vis) const { return p.whole ? 1 : tiles(vis); }
   // A segment without visible keys has one unit too: its rows are written.
   __device__ __forceinline__ int tiles(int vis) const {
     return max(1, (vis + kUnitTokens - 1) / kUnitTokens);
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       size = 0;
       if (x < n_blocks) {
         blocks.shape(x, n, len, vis, note);
-        size = blocks.tiles(vis);
+        size = blocks.weight(vis);
       }
       int incl = size;
 #pragma unroll
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       if (x0 > 0) __syncthreads();  // misc[4..7] have been read
       scan(x0, blockIdx.x == 0);
     }
-    share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
+    share = max((total + gridDim.x - 1) / gridDim.x, (long long)(p.whole ? 1 : kMinShare));
     f = share * blockIdx.x;
     f_end = min(f + share, total);
     if (n_blocks <= kThreads) {
@@ -279,12 +285,12 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     // ---- the piece: units [t0, t1) of a segment --------------------------
     const int blk = misc[8], n = misc[9], len = misc[10], vis = misc[11];
     const long long blk_at = *reinterpret_cast<long long *>(misc + 12);
-    const int tiles = blocks.tiles(vis);
-    const int h = int((f - blk_at) / tiles);
+    const int tiles = blocks.tiles(vis), weight = blocks.weight(vis);
+    const int h = int((f - blk_at) / weight);
     if (h < 0 || h >= heads) break;
-    const long long seg_at = blk_at + (long long)h * tiles;
+    const long long seg_at = blk_at + (long long)h * weight;
     const int t0 = int(f - seg_at);
-    const int t1 = int(min((long long)tiles, f_end - seg_at));
+    const int t1 = p.whole ? tiles : int(min((long long)tiles, f_end - seg_at));
     const int b = blk / blocks.row_blocks, row0 = (blk - b * blocks.row_blocks) * kRows;
     const int cells = (vis + kCellTokens - 1) / kCellTokens;
     // this warp's pairs of cells: cells 2 (p0 + 4 k) and the next, k < nk
@@ -472,6 +478,14 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       constexpr bool kMasked = decltype(masked_tag)::value;
       float sc[kF][NT][4];              // products, then scores
       uint32_t va[kF][kG], vb[kF][kG];  // V's groups of slots r, r + 8
+      uint32_t vw[kF][2][kG];           // V's codes of slots 2t, 2t + 1, and of 2t + 8, 2t + 9
+      auto load_v = [&](int x2, uint32_t cell) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int sb = 0; sb < (kG + 3) / 4; ++sb)
+            lds_words<(kG < 4 ? kG : 4)>(cell + v_word<D>(y, t, r, 4 * sb), vw[x2][y] + 4 * sb);
+      };
 #pragma unroll
       for (int x2 = 0; x2 < kF; ++x2) {
         const uint32_t cell = at + x2 * cell_bytes(D);
@@ -543,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
                      sc[x2][nt][x], sc[x2][nt][x + 1]);
         lds_words<kG>(cell + v_group<D>(r, 0), va[x2]);
         lds_words<kG>(cell + v_group<D>(r + 8, 0), vb[x2]);
+        if (FA_VE == 1) load_v(x2, cell);
         if constexpr (kMasked) {
           const int cc = c + x2;
           const bool there =
@@ -582,19 +597,21 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       weights();
 #pragma unroll
       for (int x2 = 0; x2 < kF; ++x2) {
-        float sa = kSmallStep, sb = kSmallStep;
+        // the largest p times the largest s of this thread's two slots: at
+        // least the largest p s, which is what must stay in f16's range
+        float top_s = kSmallStep;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          float s, lo;
-          unpack2<kF16>(va[x2][g], s, lo);
-          sa = fmaxf(sa, s);
-          unpack2<kF16>(vb[x2][g], s, lo);
-          sb = fmaxf(sb, s);
+          float sa, sb, lo;
+          unpack2<kF16>(va[x2][g], sa, lo);
+          unpack2<kF16>(vb[x2][g], sb, lo);
+          top_s = fmax3(top_s, sa, sb);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          over = over || fmaxf(fmaxf(pr[x2][nt][0], pr[x2][nt][1]) * sa,
-                               fmaxf(pr[x2][nt][2], pr[x2][nt][3]) * sb) > kMaxWeight;
+        for (int nt = 0; nt < NT; ++nt) {
+          const float top_p = fmaxf(fmax3(pr[x2][nt][0], pr[x2][nt][1], pr[x2][nt][2]), pr[x2][nt][3]);
+          over = over || top_p * top_s > kMaxWeight;
+        }
       }
       if (__any_sync(0xffffffffu, over)) {
         // the sizes of the tokens' values, in log2: steps, and lo as far as it
@@ -654,20 +671,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
             p2[nt][y] = f2pack(pr[x2][nt][y], pr[x2][nt][2 + y]);
             l[nt][y] += pr[x2][nt][y] + pr[x2][nt][2 + y];
           }
-        // V codes of slots 2t, 2t+1 (x = 0, 1) and 2t+8, 2t+9 (x = 2, 3)
-        constexpr int kPairs = kG / 2;
-        uint32_t vw[4][kPairs];
-        uint32_t vh[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int tok = t + 4 * x;  // cell_token(2t), (2t+1), (2t+8), (2t+9)
-          const uint32_t piece = cell + v_piece<D>(tok, r);
-          if constexpr (kPairs == 1)
-            vw[x][0] = lds32(piece);
-          else
-            lds_words<kPairs>(piece, vw[x]);
-          if constexpr (kG & 1) vh[x] = lds16(cell + v_half<D>(tok, r, kG - 1));
-        }
+        if (FA_VE == 0) load_v(x2, cell);
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
           float s0, lo0, s8, lo8;
@@ -675,15 +679,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
           unpack2<kF16>(vb[x2][g], s8, lo8);
           const uint64_t s2 = f2pack(s0, s8);
           const uint64_t mid2 = ffma2(f2pack(kMid, kMid), s2, f2pack(lo0, lo8));
-          uint32_t xa, xb;
-          if ((kG & 1) && g == kG - 1) {
-            xa = vh[0] | (vh[1] << 16);
-            xb = vh[2] | (vh[3] << 16);
-          } else {
-            const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-            xa = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-            xb = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-          }
+          const uint32_t xa = vw[x2][0][g], xb = vw[x2][1][g];
           const uint32_t xa8 = xa >> 8, xb8 = xb >> 8;
           const uint32_t ones = r == g ? 0x3c003c00u : 0u;
 #pragma unroll
@@ -725,14 +721,13 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
                                              status_code(kKernCacheFwd, 1, 1))))
         break;
       const int c = 2 * (p0 + kWarps * done);
-      const bool masked = (c + 2) * kCellTokens > all || bad_page;
+      const uint32_t at = ring + stage * kPairBytes;
+      if ((c + 2) * kCellTokens > all || bad_page) {
 #pragma unroll 1
-      for (int x = 0; x < 2; x += kF) {
-        const uint32_t at = ring + stage * kPairBytes + x * cell_bytes(D);
-        if (masked)
-          step(at, c + x, std::true_type{});
-        else
-          step(at, c + x, std::false_type{});
+        for (int x = 0; x < 2; x += kF) step(at + x * cell_bytes(D), c + x, std::true_type{});
+      } else {
+#pragma unroll kUX
+        for (int x = 0; x < 2; x += kF) step(at + x * cell_bytes(D), c + x, std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
       if (++stage == kNs) {
@@ -795,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       }
     __syncthreads();
     if (*(volatile int *)misc) {  // a wait gave up: nothing of this piece is written
-      if (threadIdx.x == 0) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 1);
+      if (threadIdx.x == 0 && !p.whole) p.chain[blockIdx.x] = make_int4(-1, 0, 0, 1);
       return;
     }
 
@@ -846,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     if (first_piece && t0 > 0) chain.w = t1 == tiles;
     first_piece = false;
 
-    f = seg_at + t1;
+    f = seg_at + (p.whole ? 1 : t1);
     if (t1 == tiles && h == heads - 1) {
       if (blk + 1 == n_blocks) break;
       if (threadIdx.x == 0) {
@@ -862,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     fence_proxy_async_smem();  // the next piece's copies overwrite the merge's reads and writes
     __syncthreads();
   }
-  if (threadIdx.x == 0) p.chain[blockIdx.x] = chain;
+  if (threadIdx.x == 0 && !p.whole) p.chain[blockIdx.x] = chain;
 }
 
 // Merge of the parts of the segments that more than one CTA worked on: block
@@ -983,7 +978,7 @@ cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
     fa_cache_fwd_kernel<D, NT, kF16><<<p.ctas, kThreads, Layout<D, NT>::kBytes, stream>>>(p);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   // set up while the attention kernel runs (programmatic dependent launch)
   LaunchProbe probe(kKindCacheCombine, stream);
   const long long rows = (long long)p.nq * p.group;
@@ -1003,9 +998,13 @@ template <int D, int NT>
 cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
   // no more CTAs than units that sequences as long as the table could have
   CacheFwdParams p = all;
-  const double units = (double)p.B * ((p.nq * p.group + 8 * NT - 1) / (8 * NT)) * p.pool.heads *
-                       ((p.pool.table_cells * kCellTokens + kUnitTokens - 1) / kUnitTokens);
-  if (units < (double)p.ctas * kMinShare) p.ctas = (int)(units + kMinShare - 1) / kMinShare;
+  const double segments =
+      (double)p.B * ((p.nq * p.group + 8 * NT - 1) / (8 * NT)) * p.pool.heads;
+  const double shares =
+      p.whole ? segments
+              : segments * ((p.pool.table_cells * kCellTokens + kUnitTokens - 1) / kUnitTokens) /
+                    kMinShare;
+  if (shares < (double)p.ctas) p.ctas = (int)shares + 1;
   return p.pool.f16 ? launch_d<D, NT, true>(p, stream) : launch_d<D, NT, false>(p, stream);
 }
 

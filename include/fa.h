@@ -371,9 +371,9 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
  * that sees no token, and rows from counts[b] on, get O = 0 and LSE = -inf.
  * B * Hq * Nq <= 2^30 - 1.
  *
- * The workspace (fa_cache_forward_workspace_bytes, 256-byte aligned) holds
- * partial results while the call runs; calls that may overlap on the GPU need
- * one each. Results do not depend on timing: equal calls on equal GPUs give
+ * The workspace (fa_cache_forward_workspace_bytes, 256-byte aligned; NULL
+ * where that is 0) holds partial results while the call runs; calls that may
+ * overlap on the GPU need one each. Results do not depend on timing: equal calls on equal GPUs give
  * equal bits.
  */
 fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,
@@ -382,10 +382,11 @@ fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int3
                            int Nq, int causal, float scale, void *workspace,
                            size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of fa_cache_forward for Hq query heads over Hk cached heads
- * and Nq query rows on the calling thread's current device (whatever the
- * batch and the lengths; 0 for invalid sizes or without a device). */
-size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d);
+/* Workspace bytes of fa_cache_forward for Hq query heads over Hk cached heads,
+ * Nq query rows and page tables of max_tokens = max_pages * page_size tokens a
+ * row, on the calling thread's current device (whatever the batch and the
+ * lengths; 0 where none is needed, for invalid sizes or without a device). */
+size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d, int max_tokens);
 
 /*
  * Debug/status query: synchronises `stream`, reads the device status word

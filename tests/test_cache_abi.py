@@ -40,7 +40,7 @@ def call_rows(lib, name="fa_cache_write", c=None, k=None, v=None, table=A, strid
     return getattr(lib, name)(c, k, v, table, stride, pages, start, counts, B, N, None)
 
 
-def call_fwd(lib, q=None, c=None, table=A, stride=4, pages=4, lengths=A, counts=None, o=None,
+def call_fwd(lib, q=None, c=None, table=A, stride=4, pages=400, lengths=A, counts=None, o=None,
              lse=A, B=3, Hq=4, Nq=5, causal=1, scale=0.1, ws=A, ws_bytes=1 << 40):
     c = cache() if c is None else c
     q = rows(H=4) if q is None else q
@@ -127,7 +127,8 @@ def test_refusals_are_explained(lib):
 
 
 def test_workspace_bytes_of_invalid_sizes(lib):
-    for bad in ((-1, 1, 1, 64), (4, 0, 1, 64), (4, 2, -1, 64), (4, 2, 1, 65)):
+    for bad in ((-1, 1, 1, 64, 4096), (4, 0, 1, 64, 4096), (4, 2, -1, 64, 4096),
+                (4, 2, 1, 65, 4096), (4, 2, 1, 64, -1), (4, 2, 1, 64, 16)):
         assert lib.fa_cache_forward_workspace_bytes(*bad) == 0
 
 

@@ -376,15 +376,15 @@ def test_results_do_not_depend_on_timing():
 def test_graph_follows_lengths_and_pages():
     """One captured step (write a token, attend) replayed as the sequences grow, then with
     other pages; two graphs with a workspace of their own each."""
-    B, H, d, page, steps = 2, 2, 64, 16, 20
+    B, H, d, page, steps, pages = 2, 2, 64, 16, 20, 64  # tables for far longer sequences
     k, v = rand((B, H, steps, d), 81, BF16), rand((B, H, steps, d), 82, BF16)
     q = rand((B, 4, steps, d), 83, BF16)
-    table, pool = random_table(B, 2, seed=8)
+    table, pool = random_table(B, pages, seed=8)
     c = new_cache(pool, H, d, page, BF16)
     kk, vv, qq = k[:, :, :1].cuda(), v[:, :, :1].cuda(), q[:, :, :1].cuda()
     tb, start, lengths = table.cuda(), ints([0, 0]), ints([1, 1])
-    ws = torch.empty(fa().cache_forward_workspace_bytes(4, H, 1, d), dtype=torch.uint8,
-                     device="cuda")
+    ws = torch.empty(fa().cache_forward_workspace_bytes(4, H, 1, d, pages * page),
+                     dtype=torch.uint8, device="cuda")
     out, lse = torch.empty_like(qq), torch.empty(B, 4, 1, device="cuda")
 
     def step():
@@ -514,7 +514,8 @@ def test_binding_refusals():
             pytest.fail(f"call {i} was taken")
     for call in (lambda: w(c, x.half(), x.half(), t, n), lambda: f(q.half(), c, t, n),
                  lambda: f(q, c, t, n, scale=-1.0),
-                 lambda: f(q, c, t, n, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
+                 lambda: f(q, c, ints([[0] * 100] * 2), n,  # long tables: sequences may be split
+                           workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(fa().FAError):
             call()
     clean()
