@@ -421,7 +421,7 @@ def cache_forward(q, cache: KVCache4, page_table, lengths, causal: bool = False,
     B, Hq, Nq, d = qs
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if out is None:
-        out = torch.empty_like(q, dtype=q.dtype if o_dtype is None else o_dtype)
+        out = torch.empty_like(q) if o_dtype is None else torch.empty_like(q, dtype=o_dtype)
     if lse is None:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     if out.shape != qs or lse.shape != (B, Hq, Nq) or \

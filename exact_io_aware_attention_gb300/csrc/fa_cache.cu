@@ -8,9 +8,12 @@
 // by at most 15 s 2^-9 (bf16), a thirtieth of a step. A group with a
 // non-finite element, or whose range overflows, is stored as s = 0, lo = NaN.
 //
-// Both kernels move each byte once: a thread owns 8 channels (16 bytes of a
-// row), four threads a group, and K and V of a row go together so that two
-// loads are in flight per thread. They are bound by HBM.
+// Both kernels move each byte once and are meant to be bound by HBM. D / 2
+// threads share a cell (16 tokens of one head): a thread owns 8 channels of
+// the tokens t, t + 4, t + 8 and t + 12, K and V, so that eight 16-byte loads
+// (or stores) are in flight per thread, the look-up of the cell is shared by
+// 64 elements, and V's words, which hold two tokens, are written whole. Four
+// neighbouring threads hold a group.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -20,182 +23,268 @@
 namespace fa {
 namespace {
 
-constexpr int kRowsPerBlock = 16;
-
-struct Place {
-  uint8_t *cell;  // null: nothing to access
-  int token;      // within the cell
-};
-
-// Where row i of (b, h) lies, recording a bad position or page once.
 template <int D>
-__device__ __forceinline__ Place find(const CacheRowsParams &p, int b, int h, int i,
-                                      uint32_t kernel) {
-  const long long pos = (long long)p.start[b] + i;
-  if (pos < 0 || pos >= (long long)p.pool.table_cells * kCellTokens) {
-    atomicCAS(p.status, 0u, index_code(kernel, 1));
-    return {nullptr, 0};
-  }
-  const int c = (int)(pos / kCellTokens);
-  const int pi = c / p.pool.page_cells;
-  const int page = p.pool.table[(size_t)((long long)b * p.pool.table_stride + pi)];
-  if (!p.pool.page_ok(page)) {
-    atomicCAS(p.status, 0u, index_code(kernel, 2));
-    return {nullptr, 0};
-  }
-  return {p.pool.template cell_ptr<D>(page, h, c - pi * p.pool.page_cells),
-          (int)(pos % kCellTokens)};
+constexpr int kCellsPerBlock = D <= 96 ? 4 : D == 128 ? 2 : 1;
+template <int D>
+constexpr int kBlock = kCellsPerBlock<D> * (D / 2);
+
+// Cells that n rows from any start can touch.
+__host__ __device__ constexpr int cells_touched(int n) {
+  return int((n + 2ll * (kCellTokens - 1)) / kCellTokens);
 }
 
-__device__ __forceinline__ int row_count(const CacheRowsParams &p, int b, uint32_t kernel) {
-  if (!p.counts) return p.n;
-  const int c = p.counts[b];
-  if (c < 0 || c > p.n) {
+// A thread's cell. Its token j is row i0 + j of (b, h); rows [0, count) are
+// cached rows, data of the cell is null where the cache has no such cell.
+struct CellTask {
+  int b, h;
+  long long i0;
+  int count;
+  uint8_t *cell;
+};
+
+// The cell of task x = (b * heads + h) * cells_touched(n) + k. A position, page
+// or count out of range is recorded.
+template <int D>
+__device__ __forceinline__ CellTask find(const CacheRowsParams &p, uint32_t x, uint32_t kernel) {
+  CellTask task;
+  const uint32_t cells = cells_touched(p.n);
+  const uint32_t bh = x / cells, k = x - bh * cells;
+  task.b = bh / p.pool.heads;
+  task.h = bh - task.b * p.pool.heads;
+  const long long start = p.start[task.b];
+  const long long c = (start >> 4) + k;  // floor, for a negative start too
+  task.i0 = c * kCellTokens - start;
+  task.count = p.counts ? p.counts[task.b] : p.n;
+  if (task.count < 0 || task.count > p.n) {
     atomicCAS(p.status, 0u, index_code(kernel, 3));
-    return c < 0 ? 0 : p.n;
+    task.count = task.count < 0 ? 0 : p.n;
   }
-  return c;
+  task.cell = nullptr;
+  if (task.i0 >= task.count || task.i0 + kCellTokens <= 0) return task;
+  if (c < 0 || c >= p.pool.table_cells) {
+    atomicCAS(p.status, 0u, index_code(kernel, 1));
+    return task;
+  }
+  const int pi = (int)c / p.pool.page_cells;
+  const int page = p.pool.table[(size_t)((long long)task.b * p.pool.table_stride + pi)];
+  if (!p.pool.page_ok(page)) {
+    atomicCAS(p.status, 0u, index_code(kernel, 2));
+    return task;
+  }
+  task.cell = p.pool.template cell_ptr<D>(page, task.h, (int)c - pi * p.pool.page_cells);
+  return task;
 }
 
 template <bool kF16>
 __device__ __forceinline__ uint32_t round16(float x) {
   return pack2<kF16>(x, 0.f) & 0xffffu;
 }
+
+// Element-wise minimum of two pairs of 16-bit values, NaN if either is.
 template <bool kF16>
-__device__ __forceinline__ float widen16(uint32_t w) {
-  float lo, hi;
-  unpack2<kF16>(w, lo, hi);
-  return lo;
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (kF16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (kF16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-// Codes of this thread's 8 channels (a quad of threads holds a group): u[i],
-// and the group word.
+// Codes of this thread's 8 channels (a quad of threads holds a group), u[i] as
+// whole floats, and the group word. Whole warps call it: the quads shuffle.
+//
+// Division is what a group would spend most of its time on, so a code comes
+// from the product with 1 / s, which is off by a few units of the last place
+// and so rounds as the quotient does except next to a tie; there (and where s
+// is not a normal number of the type, so that codes may pass 15) the thread
+// divides. 2^-16 is far above the product's error at 15 and leaves ties, one
+// element in some hundreds, to the slow path.
 template <bool kF16>
-__device__ __forceinline__ uint32_t quantise(const uint4 w, uint32_t (&u)[8]) {
-  float x[8];
-  unpack2<kF16>(w.x, x[0], x[1]);
-  unpack2<kF16>(w.y, x[2], x[3]);
-  unpack2<kF16>(w.z, x[4], x[5]);
-  unpack2<kF16>(w.w, x[6], x[7]);
-  float lo = x[0], hi = x[0], z = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    z = fmaf(x[i], 0.f, z);  // NaN if any element is not finite
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
+__device__ __forceinline__ uint32_t quantise(const uint4 w, float (&u)[8]) {
+  uint32_t low = min2_nan<kF16>(min2_nan<kF16>(w.x, w.y), min2_nan<kF16>(w.z, w.w));
+  uint32_t high = max2_nan<kF16>(max2_nan<kF16>(w.x, w.y), max2_nan<kF16>(w.z, w.w));
+  low = min2_nan<kF16>(low, __byte_perm(low, low, 0x1032));
+  high = max2_nan<kF16>(high, __byte_perm(high, high, 0x1032));
+  // (min, -max) in one word for the quad
+  uint32_t both = __byte_perm(low, high ^ 0x80008000u, 0x5410);
+  both = min2_nan<kF16>(both, __shfl_xor_sync(0xffffffffu, both, 1));
+  both = min2_nan<kF16>(both, __shfl_xor_sync(0xffffffffu, both, 2));
+  float lo, hi;
+  unpack2<kF16>(both ^ 0x80000000u, lo, hi);
   const uint32_t s16 = round16<kF16>(__fdiv_rn(hi - lo, 15.f));
-  const float s = widen16<kF16>(s16);
-  const bool bad = !(z == 0.f) || !(s < INFINITY);
-  const bool flat = bad || !(s > 0.f);
+  float s, unused;
+  unpack2<kF16>(s16, s, unused);
+  float d[8];
+  unpack2<kF16>(w.x, d[0], d[1]);
+  unpack2<kF16>(w.y, d[2], d[3]);
+  unpack2<kF16>(w.z, d[4], d[5]);
+  unpack2<kF16>(w.w, d[6], d[7]);
+  const float inv = __frcp_rn(s);
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+  float worst = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = flat ? 0.f : fminf(rintf(__fdiv_rn(x[i] - lo, s)), 15.f);
-    u[i] = (uint32_t)(int)q;
+    d[i] -= lo;
+    u[i] = fmaf(d[i], inv, kRound) - kRound;
+    worst = fmaxf(worst, fabsf(fmaf(d[i], inv, -u[i])));
   }
-  return bad ? 0x7fff0000u : (s16 | (round16<kF16>(lo) << 16));
+  constexpr float kNormal = kF16 ? 0x1p-14f : 0x1p-126f;
+  if (worst > 0.5f - 0x1p-16f || !(s >= kNormal && s < INFINITY)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      u[i] = s > 0.f && s < INFINITY ? fminf(rintf(__fdiv_rn(d[i], s)), 15.f) : 0.f;
+    if (!(s < INFINITY)) return 0x7fff0000u;
+  }
+  return s16 | ((both & 0xffffu) << 16);
+}
+
+// Four codes as the nibbles of 16 bits (exact in fp32), code 0 lowest.
+__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
+  const float v = fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a);
+  return __float_as_uint(v + 8388608.f) & 0xffffu;  // 2^23: the sum's last bits are v
 }
 
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kRowsPerBlock *(D / 8))
+__global__ void __launch_bounds__(kBlock<D>)
     fa_cache_write_kernel(const __grid_constant__ CacheRowsParams p) {
   constexpr int kLanes = D / 8;
-  const int lr = threadIdx.x / kLanes, part = threadIdx.x % kLanes;
+  const int in_cell = threadIdx.x % (D / 2);
+  const int tok = in_cell / kLanes, part = in_cell % kLanes;  // tokens tok + 4 x
   const int g = part >> 2, t = part & 3;
-  const uint32_t row = blockIdx.x * kRowsPerBlock + lr;  // (b * heads + h) * n + i
-  const uint32_t rows = (uint32_t)p.B * p.pool.heads * p.n;
-  const bool in = row < rows;
-  const uint32_t bh = in ? row / p.n : 0, i = in ? row - bh * p.n : 0;
-  const int b = bh / p.pool.heads, h = bh - b * p.pool.heads;
-  const bool live = in && (int)i < row_count(p, b, kKernCacheWrite);
-  Place at = {nullptr, 0};
-  if (live) at = find<D>(p, b, h, i, kKernCacheWrite);
-  uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
-  if (at.cell) {
-    const uint16_t *k = static_cast<const uint16_t *>(p.k), *v = static_cast<const uint16_t *>(p.v);
-    wk = *reinterpret_cast<const uint4 *>(k + p.sk.row(b, h, i) + part * 8);
-    wv = *reinterpret_cast<const uint4 *>(v + p.sv.row(b, h, i) + part * 8);
-  }
-  uint32_t uk[8], uv[8];
-  const uint32_t gk = quantise<kF16>(wk, uk);  // (whole warps: the quads shuffle)
-  const uint32_t gv = quantise<kF16>(wv, uv);
-  uint32_t kw = 0, v0 = 0, v1 = 0;
+  const uint32_t x = blockIdx.x * kCellsPerBlock<D> + threadIdx.x / (D / 2);
+  const uint32_t tasks = (uint32_t)p.B * p.pool.heads * cells_touched(p.n);
+  CellTask task;
+  task.cell = nullptr;
+  if (x < tasks) task = find<D>(p, x, kKernCacheWrite);
+  uint4 wk[4], wv[4];
+  bool live[4];
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    kw |= (uk[2 * x] << (4 * x)) | (uk[2 * x + 1] << (16 + 4 * x));
-    v0 |= uv[x] << (4 * x);      // halfword r = 2t
-    v1 |= uv[4 + x] << (4 * x);  // halfword r = 2t + 1
+  for (int j = 0; j < 4; ++j) {
+    const long long i = task.cell ? task.i0 + tok + 4 * j : -1;
+    live[j] = task.cell && i >= 0 && i < task.count;
+    wk[j] = wv[j] = make_uint4(0, 0, 0, 0);
+    if (live[j]) {
+      wk[j] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.k) +
+                                                     p.sk.row(task.b, task.h, (int)i) + part * 8));
+      wv[j] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.v) +
+                                                     p.sv.row(task.b, task.h, (int)i) + part * 8));
+    }
   }
-  const int slot = cell_slot(at.token);
-  if (!at.cell) return;
-  *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t, g)) = (uint16_t)v0;
-  *reinterpret_cast<uint16_t *>(at.cell + v_half<D>(at.token, 2 * t + 1, g)) = (uint16_t)v1;
-  *reinterpret_cast<uint32_t *>(at.cell + k_word<D>(slot, t, g)) = kw;
-  if (t == 0) *reinterpret_cast<uint32_t *>(at.cell + k_group<D>(slot, g)) = gk;
-  if (t == 1) *reinterpret_cast<uint32_t *>(at.cell + v_group<D>(slot, g)) = gv;
+  if (!__any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3])) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float u[8];
+    const uint32_t group = quantise<kF16>(wk[j], u);
+    const uint32_t word = nibbles(u[0], u[2], u[4], u[6]) | (nibbles(u[1], u[3], u[5], u[7]) << 16);
+    const int slot = cell_slot(tok + 4 * j);
+    if (live[j]) {
+      *reinterpret_cast<uint32_t *>(task.cell + k_word<D>(slot, t, g)) = word;
+      if (t == 0) *reinterpret_cast<uint32_t *>(task.cell + k_group<D>(slot, g)) = group;
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {  // tokens tok + 8 y and tok + 8 y + 4
+    uint32_t half[2][2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      float u[8];
+      const uint32_t group = quantise<kF16>(wv[2 * y + z], u);
+      half[z][0] = nibbles(u[0], u[1], u[2], u[3]);  // r = 2 t
+      half[z][1] = nibbles(u[4], u[5], u[6], u[7]);  // r = 2 t + 1
+      if (live[2 * y + z] && t == 1)
+        *reinterpret_cast<uint32_t *>(task.cell + v_group<D>(cell_slot(tok + 8 * y + 4 * z), g)) =
+            group;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint8_t *const at = task.cell + v_word<D>(y, tok, 2 * t + q, g);
+      if (live[2 * y] && live[2 * y + 1])
+        *reinterpret_cast<uint32_t *>(at) = half[0][q] | (half[1][q] << 16);
+      else if (live[2 * y])
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)half[0][q];
+      else if (live[2 * y + 1])
+        *reinterpret_cast<uint16_t *>(at + 2) = (uint16_t)half[1][q];
+    }
+  }
 }
 
-// lo + s u rounded once to the 16-bit type (s u is exact in fp32).
+// lo + s u rounded once to the 16-bit type (s u is exact in fp32), for two codes.
 template <bool kF16>
 __device__ __forceinline__ uint32_t value2(uint32_t ua, uint32_t ub, float s, float lo) {
-  return pack2<kF16>(fmaf((float)ua, s, lo), fmaf((float)ub, s, lo));
+  // 2^23 + u as a float, minus 2^23: no conversion instruction
+  const float a = __uint_as_float(0x4b000000u | ua) - 8388608.f;
+  const float b = __uint_as_float(0x4b000000u | ub) - 8388608.f;
+  return pack2<kF16>(fmaf(a, s, lo), fmaf(b, s, lo));
 }
 
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kRowsPerBlock *(D / 8))
+__global__ void __launch_bounds__(kBlock<D>)
     fa_cache_read_kernel(const __grid_constant__ CacheRowsParams p) {
   constexpr int kLanes = D / 8;
-  const int lr = threadIdx.x / kLanes, part = threadIdx.x % kLanes;
+  const int in_cell = threadIdx.x % (D / 2);
+  const int tok = in_cell / kLanes, part = in_cell % kLanes;  // tokens tok + 4 x
   const int g = part >> 2, t = part & 3;
-  const uint32_t row = blockIdx.x * kRowsPerBlock + lr;
-  const uint32_t rows = (uint32_t)p.B * p.pool.heads * p.n;
-  if (row >= rows) return;
-  const uint32_t bh = row / p.n, i = row - bh * p.n;
-  const int b = bh / p.pool.heads, h = bh - b * p.pool.heads;
-  Place at = {nullptr, 0};
-  if ((int)i < row_count(p, b, kKernCacheRead)) at = find<D>(p, b, h, i, kKernCacheRead);
-  uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;  // rows without a token read zero
-  if (at.cell) {
-    const int slot = cell_slot(at.token);
-    const uint32_t kw = *reinterpret_cast<const uint32_t *>(at.cell + k_word<D>(slot, t, g));
-    const uint32_t gk = *reinterpret_cast<const uint32_t *>(at.cell + k_group<D>(slot, g));
-    const uint32_t gv = *reinterpret_cast<const uint32_t *>(at.cell + v_group<D>(slot, g));
-    const uint32_t v0 = *reinterpret_cast<const uint16_t *>(at.cell + v_half<D>(at.token, 2 * t, g));
-    const uint32_t v1 =
-        *reinterpret_cast<const uint16_t *>(at.cell + v_half<D>(at.token, 2 * t + 1, g));
-    float s, lo;
-    unpack2<kF16>(gk, s, lo);
-    wk.x = value2<kF16>(kw & 15, (kw >> 16) & 15, s, lo);
-    wk.y = value2<kF16>((kw >> 4) & 15, (kw >> 20) & 15, s, lo);
-    wk.z = value2<kF16>((kw >> 8) & 15, (kw >> 24) & 15, s, lo);
-    wk.w = value2<kF16>((kw >> 12) & 15, (kw >> 28) & 15, s, lo);
-    unpack2<kF16>(gv, s, lo);
-    wv.x = value2<kF16>(v0 & 15, (v0 >> 4) & 15, s, lo);
-    wv.y = value2<kF16>((v0 >> 8) & 15, (v0 >> 12) & 15, s, lo);
-    wv.z = value2<kF16>(v1 & 15, (v1 >> 4) & 15, s, lo);
-    wv.w = value2<kF16>((v1 >> 8) & 15, (v1 >> 12) & 15, s, lo);
+  const uint32_t x = blockIdx.x * kCellsPerBlock<D> + threadIdx.x / (D / 2);
+  const uint32_t tasks = (uint32_t)p.B * p.pool.heads * cells_touched(p.n);
+  if (x >= tasks) return;
+  const CellTask task = find<D>(p, x, kKernCacheRead);
+  uint32_t kw[4] = {}, gk[4] = {}, gv[4] = {}, vw[2][2] = {};
+  if (task.cell) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = cell_slot(tok + 4 * j);
+      kw[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + k_word<D>(slot, t, g)));
+      gk[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + k_group<D>(slot, g)));
+      gv[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + v_group<D>(slot, g)));
+      vw[j >> 1][j & 1] = __ldg(reinterpret_cast<const uint32_t *>(
+          task.cell + v_word<D>(j >> 1, tok, 2 * t + (j & 1), g)));
+    }
   }
-  uint16_t *k = static_cast<uint16_t *>(p.k), *v = static_cast<uint16_t *>(p.v);
-  *reinterpret_cast<uint4 *>(k + p.sk.row(b, h, i) + part * 8) = wk;
-  *reinterpret_cast<uint4 *>(v + p.sv.row(b, h, i) + part * 8) = wv;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const long long i = task.i0 + tok + 4 * j;
+    if (i < 0 || i >= p.n) continue;
+    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;  // rows without a token read zero
+    if (task.cell && i < task.count) {
+      float s, lo;
+      unpack2<kF16>(gk[j], s, lo);
+      const uint32_t c = kw[j];
+      wk.x = value2<kF16>(c & 15, (c >> 16) & 15, s, lo);
+      wk.y = value2<kF16>((c >> 4) & 15, (c >> 20) & 15, s, lo);
+      wk.z = value2<kF16>((c >> 8) & 15, (c >> 24) & 15, s, lo);
+      wk.w = value2<kF16>((c >> 12) & 15, c >> 28, s, lo);
+      unpack2<kF16>(gv[j], s, lo);
+      const uint32_t a = vw[j >> 1][0] >> (16 * (j & 1)), b = vw[j >> 1][1] >> (16 * (j & 1));
+      wv.x = value2<kF16>(a & 15, (a >> 4) & 15, s, lo);
+      wv.y = value2<kF16>((a >> 8) & 15, (a >> 12) & 15, s, lo);
+      wv.z = value2<kF16>(b & 15, (b >> 4) & 15, s, lo);
+      wv.w = value2<kF16>((b >> 8) & 15, (b >> 12) & 15, s, lo);
+    }
+    uint16_t *k = static_cast<uint16_t *>(p.k), *v = static_cast<uint16_t *>(p.v);
+    *reinterpret_cast<uint4 *>(k + p.sk.row(task.b, task.h, (int)i) + part * 8) = wk;
+    *reinterpret_cast<uint4 *>(v + p.sv.row(task.b, task.h, (int)i) + part * 8) = wv;
+  }
 }
 
 template <int D, bool kF16>
 cudaError_t launch_rows(const CacheRowsParams &p, bool write, cudaStream_t stream) {
-  const uint32_t rows = (uint32_t)p.B * p.pool.heads * p.n;
-  const unsigned grid = rows / kRowsPerBlock + (rows % kRowsPerBlock != 0);
-  const unsigned block = kRowsPerBlock * (D / 8);
+  const uint32_t tasks = (uint32_t)p.B * p.pool.heads * cells_touched(p.n);
+  const unsigned grid = (tasks - 1) / kCellsPerBlock<D> + 1;
   LaunchProbe probe(write ? kKindCacheWrite : kKindCacheRead, stream);
   if (write)
-    fa_cache_write_kernel<D, kF16><<<grid, block, 0, stream>>>(p);
+    fa_cache_write_kernel<D, kF16><<<grid, kBlock<D>, 0, stream>>>(p);
   else
-    fa_cache_read_kernel<D, kF16><<<grid, block, 0, stream>>>(p);
+    fa_cache_read_kernel<D, kF16><<<grid, kBlock<D>, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
