@@ -100,17 +100,38 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Codes of this thread's 8 channels (a quad of threads holds a group), u[i] as
-// whole floats, and the group word. Whole warps call it: the quads shuffle.
-//
-// Division is what a group would spend most of its time on, so a code comes
-// from the product with 1 / s, which is off by a few units of the last place
-// and so rounds as the quotient does except next to a tie; there (and where s
-// is not a normal number of the type, so that codes may pass 15) the thread
-// divides. 2^-16 is far above the product's error at 15 and leaves ties, one
-// element in some hundreds, to the slow path.
+// Four codes as the nibbles of 16 bits (exact in fp32), code 0 lowest.
+__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
+  const float v = fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a);
+  return __float_as_uint(v + 8388608.f) & 0xffffu;  // 2^23: the sum's last bits are v
+}
+
+// Codes by division: for groups whose range or step is near the ends of the
+// exponents, or not finite, or where the type's subnormals make the step so
+// coarse that a code passes 15. Out of line, being rare.
+__device__ __noinline__ uint32_t codes_by_division(float4 a, float4 b, float s) {
+  const float d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    u[i] = s > 0.f && s < INFINITY ? fminf(rintf(__fdiv_rn(d[i], s)), 15.f) : 0.f;
+  return nibbles(u[0], u[1], u[2], u[3]) | (nibbles(u[4], u[5], u[6], u[7]) << 16);
+}
+
+// The correctly rounded quotient a / b of normal numbers from inv = rn(1 / b),
+// by one correction with the remainder (Markstein, IBM J. Res. Dev. 34, 1990):
+// y = rn(a inv) is within two units of the last place, so r = a - y b is exact
+// for a b of few bits (11 here), and y + r inv differs from a / b by 2^-47 of it,
+// less than the distance of a quotient by 11 bits from the middle of two floats.
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+  const float y = a * inv;
+  return fmaf(fmaf(-y, b, a), inv, y);
+}
+
+// Codes of this thread's 8 channels (a quad of threads holds a group) as the
+// nibbles of a word, and the group word. Whole warps call it: the quads shuffle.
 template <bool kF16>
-__device__ __forceinline__ uint32_t quantise(const uint4 w, float (&u)[8]) {
+__device__ __forceinline__ uint32_t quantise(const uint4 w, uint32_t &group) {
   uint32_t low = min2_nan<kF16>(min2_nan<kF16>(w.x, w.y), min2_nan<kF16>(w.z, w.w));
   uint32_t high = max2_nan<kF16>(max2_nan<kF16>(w.x, w.y), max2_nan<kF16>(w.z, w.w));
   low = min2_nan<kF16>(low, __byte_perm(low, low, 0x1032));
@@ -121,37 +142,34 @@ __device__ __forceinline__ uint32_t quantise(const uint4 w, float (&u)[8]) {
   both = min2_nan<kF16>(both, __shfl_xor_sync(0xffffffffu, both, 2));
   float lo, hi;
   unpack2<kF16>(both ^ 0x80000000u, lo, hi);
-  const uint32_t s16 = round16<kF16>(__fdiv_rn(hi - lo, 15.f));
-  float s, unused;
-  unpack2<kF16>(s16, s, unused);
   float d[8];
   unpack2<kF16>(w.x, d[0], d[1]);
   unpack2<kF16>(w.y, d[2], d[3]);
   unpack2<kF16>(w.z, d[4], d[5]);
   unpack2<kF16>(w.w, d[6], d[7]);
-  const float inv = __frcp_rn(s);
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-  float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    d[i] -= lo;
-    u[i] = fmaf(d[i], inv, kRound) - kRound;
-    worst = fmaxf(worst, fabsf(fmaf(d[i], inv, -u[i])));
-  }
-  constexpr float kNormal = kF16 ? 0x1p-14f : 0x1p-126f;
-  if (worst > 0.5f - 0x1p-16f || !(s >= kNormal && s < INFINITY)) {
+  for (int i = 0; i < 8; ++i) d[i] -= lo;
+  const float range = hi - lo;
+  float s, unused;
+  // s at least the type's smallest normal number (2^-14 for f16, whose largest
+  // range is 2^17), and everything far from the ends of fp32's exponents
+  constexpr float kFrom = kF16 ? 0x1p-10f : 0x1p-96f, kTo = 0x1p96f;
+  if (range >= kFrom && range <= kTo) {
+    const uint32_t s16 = round16<kF16>(quotient(range, 15.f, 1.f / 15.f));
+    unpack2<kF16>(s16, s, unused);
+    const float inv = __frcp_rn(s);
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+    float u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      u[i] = s > 0.f && s < INFINITY ? fminf(rintf(__fdiv_rn(d[i], s)), 15.f) : 0.f;
-    if (!(s < INFINITY)) return 0x7fff0000u;
+    for (int i = 0; i < 8; ++i) u[i] = (quotient(d[i], s, inv) + kRound) - kRound;
+    group = s16 | ((both & 0xffffu) << 16);
+    return nibbles(u[0], u[1], u[2], u[3]) | (nibbles(u[4], u[5], u[6], u[7]) << 16);
   }
-  return s16 | ((both & 0xffffu) << 16);
-}
-
-// Four codes as the nibbles of 16 bits (exact in fp32), code 0 lowest.
-__device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
-  const float v = fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a);
-  return __float_as_uint(v + 8388608.f) & 0xffffu;  // 2^23: the sum's last bits are v
+  const uint32_t s16 = round16<kF16>(__fdiv_rn(range, 15.f));
+  unpack2<kF16>(s16, s, unused);
+  group = s < INFINITY ? s16 | ((both & 0xffffu) << 16) : 0x7fff0000u;
+  return codes_by_division(make_float4(d[0], d[1], d[2], d[3]),
+                           make_float4(d[4], d[5], d[6], d[7]), s);
 }
 
 template <int D, bool kF16>
@@ -183,9 +201,8 @@ __global__ void __launch_bounds__(kBlock<D>)
   if (!__any_sync(0xffffffffu, live[0] || live[1] || live[2] || live[3])) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float u[8];
-    const uint32_t group = quantise<kF16>(wk[j], u);
-    const uint32_t word = nibbles(u[0], u[2], u[4], u[6]) | (nibbles(u[1], u[3], u[5], u[7]) << 16);
+    uint32_t group;
+    const uint32_t word = quantise<kF16>(wk[j], group);
     const int slot = cell_slot(tok + 4 * j);
     if (live[j]) {
       *reinterpret_cast<uint32_t *>(task.cell + k_word<D>(slot, t, g)) = word;
@@ -194,13 +211,11 @@ __global__ void __launch_bounds__(kBlock<D>)
   }
 #pragma unroll
   for (int y = 0; y < 2; ++y) {  // tokens tok + 8 y and tok + 8 y + 4
-    uint32_t half[2][2];
+    uint32_t word[2];  // its halves are those of r = 2 t and r = 2 t + 1
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      float u[8];
-      const uint32_t group = quantise<kF16>(wv[2 * y + z], u);
-      half[z][0] = nibbles(u[0], u[1], u[2], u[3]);  // r = 2 t
-      half[z][1] = nibbles(u[4], u[5], u[6], u[7]);  // r = 2 t + 1
+      uint32_t group;
+      word[z] = quantise<kF16>(wv[2 * y + z], group);
       if (live[2 * y + z] && t == 1)
         *reinterpret_cast<uint32_t *>(task.cell + v_group<D>(cell_slot(tok + 8 * y + 4 * z), g)) =
             group;
@@ -209,11 +224,11 @@ __global__ void __launch_bounds__(kBlock<D>)
     for (int q = 0; q < 2; ++q) {
       uint8_t *const at = task.cell + v_word<D>(y, tok, 2 * t + q, g);
       if (live[2 * y] && live[2 * y + 1])
-        *reinterpret_cast<uint32_t *>(at) = half[0][q] | (half[1][q] << 16);
+        *reinterpret_cast<uint32_t *>(at) = __byte_perm(word[0], word[1], q ? 0x7632 : 0x5410);
       else if (live[2 * y])
-        *reinterpret_cast<uint16_t *>(at) = (uint16_t)half[0][q];
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)(word[0] >> (16 * q));
       else if (live[2 * y + 1])
-        *reinterpret_cast<uint16_t *>(at + 2) = (uint16_t)half[1][q];
+        *reinterpret_cast<uint16_t *>(at + 2) = (uint16_t)(word[1] >> (16 * q));
     }
   }
 }
@@ -259,10 +274,10 @@ __global__ void __launch_bounds__(kBlock<D>)
       float s, lo;
       unpack2<kF16>(gk[j], s, lo);
       const uint32_t c = kw[j];
-      wk.x = value2<kF16>(c & 15, (c >> 16) & 15, s, lo);
-      wk.y = value2<kF16>((c >> 4) & 15, (c >> 20) & 15, s, lo);
-      wk.z = value2<kF16>((c >> 8) & 15, (c >> 24) & 15, s, lo);
-      wk.w = value2<kF16>((c >> 12) & 15, c >> 28, s, lo);
+      wk.x = value2<kF16>(c & 15, (c >> 4) & 15, s, lo);
+      wk.y = value2<kF16>((c >> 8) & 15, (c >> 12) & 15, s, lo);
+      wk.z = value2<kF16>((c >> 16) & 15, (c >> 20) & 15, s, lo);
+      wk.w = value2<kF16>((c >> 24) & 15, c >> 28, s, lo);
       unpack2<kF16>(gv[j], s, lo);
       const uint32_t a = vw[j >> 1][0] >> (16 * (j & 1)), b = vw[j >> 1][1] >> (16 * (j & 1));
       wv.x = value2<kF16>(a & 15, (a >> 4) & 15, s, lo);

@@ -18,8 +18,8 @@
 //
 //   token j of a cell is matrix row cell_slot(j); K codes and both group
 //   arrays are in slot order;
-//   K: channel c = 32 g + 8 t + i is nibble i/2 of the (i%2)-th half of word
-//   (t, g): the halves are the two k-neighbours of the product;
+//   K: channel c = 32 g + 8 t + i is nibble i of word (t, g); channels i and
+//   i + 4, in the two halves, are k-neighbours of the product;
 //   V: channel c = 32 g + 4 r + i of tokens t + 8 y and t + 8 y + 4, which are
 //   k-neighbours, is nibble i of the halves of word (y, t, r, g).
 #pragma once

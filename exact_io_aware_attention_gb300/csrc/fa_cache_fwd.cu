@@ -357,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 
     // ---- Q as the B operand of S^T -----------------------------------------
     // Thread (r, t) holds, of query row r of each n-tile, channels 8 t .. 8 t + 7
-    // of every group: pairs (0,1), (2,3) for the group's first 16-deep product,
-    // (4,5), (6,7) for the second; the pairs that meet nibbles 1 and 3 of a
-    // word (codes * 2^-20) are scaled by 2^-4. qs: the sums of q over the
+    // of every group: pairs (0,4), (1,5) for the group's first 16-deep product,
+    // (2,6), (3,7) for the second; the pairs that meet nibbles 1 and 3 of a
+    // half word (codes * 2^-20) are scaled by 2^-4. qs: the sums of q over the
     // groups as the B operand of the product with lo, whose 16 columns are the
     // groups (two, four or eight) repeated, with one term of a sum each.
     constexpr int kGp = kG == 3 ? 4 : kG;
@@ -404,13 +404,14 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       float sum[kGp] = {};
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        const uint32_t in[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+        float q8[8];
+        unpack2<kF16>(w[g].x, q8[0], q8[1]);
+        unpack2<kF16>(w[g].y, q8[2], q8[3]);
+        unpack2<kF16>(w[g].z, q8[4], q8[5]);
+        unpack2<kF16>(w[g].w, q8[6], q8[7]);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float a, c;
-          unpack2<kF16>(in[x], a, c);
-          a = finite ? a * up : 0.f;
-          c = finite ? c * up : 0.f;
+          const float a = finite ? q8[x] * up : 0.f, c = finite ? q8[x + 4] * up : 0.f;
           sum[g] += a + c;
           const float f4 = (x & 1) ? 0x1p-4f : 1.f;
           qb[nt][g][x] = pack_f16x2(a * f4, c * f4);
