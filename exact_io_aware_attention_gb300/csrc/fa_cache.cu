@@ -118,11 +118,16 @@ __device__ __noinline__ uint32_t codes_by_division(float4 a, float4 b, float s) 
   return nibbles(u[0], u[1], u[2], u[3]) | (nibbles(u[4], u[5], u[6], u[7]) << 16);
 }
 
-// The correctly rounded quotient a / b of normal numbers from inv = rn(1 / b),
-// by one correction with the remainder (Markstein, IBM J. Res. Dev. 34, 1990):
-// y = rn(a inv) is within two units of the last place, so r = a - y b is exact
-// for a b of few bits (11 here), and y + r inv differs from a / b by 2^-47 of it,
-// less than the distance of a quotient by 11 bits from the middle of two floats.
+// The correctly rounded quotients a / b of normal numbers from inv, 1 / b to a
+// few units of the last place, by one correction with the remainder (Markstein,
+// IBM J. Res. Dev. 34, 1990): y = rn(a inv) is within 2^-21 of the quotient, so
+// r = a - y b is exact for a b of few bits (11 here), and y + r inv differs
+// from a / b by 2^-43 of it, less than the distance of a quotient by 11 bits
+// from the middle of two floats (2^-36).
+__device__ __forceinline__ uint64_t quotient2(uint64_t a, uint64_t neg_b, uint64_t inv) {
+  const uint64_t y = fmul2(a, inv);
+  return ffma2(ffma2(y, neg_b, a), inv, y);
+}
 __device__ __forceinline__ float quotient(float a, float b, float inv) {
   const float y = a * inv;
   return fmaf(fmaf(-y, b, a), inv, y);
@@ -142,13 +147,16 @@ __device__ __forceinline__ uint32_t quantise(const uint4 w, uint32_t &group) {
   both = min2_nan<kF16>(both, __shfl_xor_sync(0xffffffffu, both, 2));
   float lo, hi;
   unpack2<kF16>(both ^ 0x80000000u, lo, hi);
+  // x - lo, in pairs of channels i and i + 4, whose codes fill the two halves
   float d[8];
   unpack2<kF16>(w.x, d[0], d[1]);
   unpack2<kF16>(w.y, d[2], d[3]);
   unpack2<kF16>(w.z, d[4], d[5]);
   unpack2<kF16>(w.w, d[6], d[7]);
+  const uint64_t lo2 = f2pack(lo, lo);
+  uint64_t d2[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] -= lo;
+  for (int i = 0; i < 4; ++i) d2[i] = fsub2(f2pack(d[i], d[i + 4]), lo2);
   const float range = hi - lo;
   float s, unused;
   // s at least the type's smallest normal number (2^-14 for f16, whose largest
@@ -157,17 +165,25 @@ __device__ __forceinline__ uint32_t quantise(const uint4 w, uint32_t &group) {
   if (range >= kFrom && range <= kTo) {
     const uint32_t s16 = round16<kF16>(quotient(range, 15.f, 1.f / 15.f));
     unpack2<kF16>(s16, s, unused);
-    const float inv = __frcp_rn(s);
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-    float u[8];
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint64_t inv2 = f2pack(inv, inv), neg2 = f2pack(-s, -s);
+    const uint64_t round2 = f2pack(12582912.f, 12582912.f);  // adding 1.5 * 2^23 rounds to whole
+    uint64_t u[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = (quotient(d[i], s, inv) + kRound) - kRound;
-    group = s16 | ((both & 0xffffu) << 16);
-    return nibbles(u[0], u[1], u[2], u[3]) | (nibbles(u[4], u[5], u[6], u[7]) << 16);
+    for (int i = 0; i < 4; ++i) u[i] = fsub2(fadd2(quotient2(d2[i], neg2, inv2), round2), round2);
+    const uint64_t sixteen2 = f2pack(16.f, 16.f);
+    uint64_t v = ffma2(ffma2(ffma2(u[3], sixteen2, u[2]), sixteen2, u[1]), sixteen2, u[0]);
+    float v0, v1;
+    f2unpack(fadd2(v, f2pack(8388608.f, 8388608.f)), v0, v1);  // 2^23: the last bits are the codes
+    group = s16 | (both << 16);
+    return __byte_perm(__float_as_uint(v0), __float_as_uint(v1), 0x5410);
   }
   const uint32_t s16 = round16<kF16>(__fdiv_rn(range, 15.f));
   unpack2<kF16>(s16, s, unused);
-  group = s < INFINITY ? s16 | ((both & 0xffffu) << 16) : 0x7fff0000u;
+  group = s < INFINITY ? s16 | (both << 16) : 0x7fff0000u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2unpack(d2[i], d[i], d[i + 4]);
   return codes_by_division(make_float4(d[0], d[1], d[2], d[3]),
                            make_float4(d[4], d[5], d[6], d[7]), s);
 }
