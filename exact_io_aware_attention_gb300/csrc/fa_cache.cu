@@ -222,30 +222,30 @@ __global__ void __launch_bounds__(kBlock<D>)
     const int slot = cell_slot(tok + 4 * j);
     if (live[j]) {
       *reinterpret_cast<uint32_t *>(task.cell + k_word<D>(slot, t, g)) = word;
-      if (t == 0) *reinterpret_cast<uint32_t *>(task.cell + k_group<D>(slot, g)) = group;
+      if (t == 0) *reinterpret_cast<uint16_t *>(task.cell + k_s<D>(slot, g)) = (uint16_t)group;
+      if (t == 1) *reinterpret_cast<uint16_t *>(task.cell + k_lo<D>(slot, g)) = (uint16_t)(group >> 16);
     }
   }
 #pragma unroll
   for (int y = 0; y < 2; ++y) {  // tokens tok + 8 y and tok + 8 y + 4
-    uint32_t word[2];  // its halves are those of r = 2 t and r = 2 t + 1
+    // codes, whose halves are those of r = 2 t and r = 2 t + 1, and groups
+    uint32_t word[2], group[2];
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      uint32_t group;
-      word[z] = quantise<kF16>(wv[2 * y + z], group);
-      if (live[2 * y + z] && t == 1)
-        *reinterpret_cast<uint32_t *>(task.cell + v_group<D>(cell_slot(tok + 8 * y + 4 * z), g)) =
-            group;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint8_t *const at = task.cell + v_word<D>(y, tok, 2 * t + q, g);
+    for (int z = 0; z < 2; ++z) word[z] = quantise<kF16>(wv[2 * y + z], group[z]);
+    // the low (q = 0) or high halves of a pair of words, to the pair's tokens
+    auto store = [&](int off, const uint32_t (&w)[2], int q) {
+      uint8_t *const at = task.cell + off;
       if (live[2 * y] && live[2 * y + 1])
-        *reinterpret_cast<uint32_t *>(at) = __byte_perm(word[0], word[1], q ? 0x7632 : 0x5410);
+        *reinterpret_cast<uint32_t *>(at) = __byte_perm(w[0], w[1], q ? 0x7632 : 0x5410);
       else if (live[2 * y])
-        *reinterpret_cast<uint16_t *>(at) = (uint16_t)(word[0] >> (16 * q));
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)(w[0] >> (16 * q));
       else if (live[2 * y + 1])
-        *reinterpret_cast<uint16_t *>(at + 2) = (uint16_t)(word[1] >> (16 * q));
-    }
+        *reinterpret_cast<uint16_t *>(at + 2) = (uint16_t)(w[1] >> (16 * q));
+    };
+    store(v_word<D>(y, tok, 2 * t, g), word, 0);
+    store(v_word<D>(y, tok, 2 * t + 1, g), word, 1);
+    if (t == 2) store(v_s<D>(y, tok, g), group, 0);
+    if (t == 3) store(v_lo<D>(y, tok, g), group, 1);
   }
 }
 
@@ -269,16 +269,21 @@ __global__ void __launch_bounds__(kBlock<D>)
   const uint32_t tasks = (uint32_t)p.B * p.pool.heads * cells_touched(p.n);
   if (x >= tasks) return;
   const CellTask task = find<D>(p, x, kKernCacheRead);
-  uint32_t kw[4] = {}, gk[4] = {}, gv[4] = {}, vw[2][2] = {};
+  uint32_t kw[4] = {}, gk[4] = {}, vw[2][2] = {}, vs[2] = {}, vl[2] = {};
   if (task.cell) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int slot = cell_slot(tok + 4 * j);
       kw[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + k_word<D>(slot, t, g)));
-      gk[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + k_group<D>(slot, g)));
-      gv[j] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + v_group<D>(slot, g)));
+      gk[j] = __ldg(reinterpret_cast<const uint16_t *>(task.cell + k_s<D>(slot, g))) |
+              ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(task.cell + k_lo<D>(slot, g))) << 16);
       vw[j >> 1][j & 1] = __ldg(reinterpret_cast<const uint32_t *>(
           task.cell + v_word<D>(j >> 1, tok, 2 * t + (j & 1), g)));
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      vs[y] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + v_s<D>(y, tok, g)));
+      vl[y] = __ldg(reinterpret_cast<const uint32_t *>(task.cell + v_lo<D>(y, tok, g)));
     }
   }
 #pragma unroll
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kBlock<D>)
       wk.y = value2<kF16>((c >> 8) & 15, (c >> 12) & 15, s, lo);
       wk.z = value2<kF16>((c >> 16) & 15, (c >> 20) & 15, s, lo);
       wk.w = value2<kF16>((c >> 24) & 15, c >> 28, s, lo);
-      unpack2<kF16>(gv[j], s, lo);
+      unpack2<kF16>(__byte_perm(vs[j >> 1], vl[j >> 1], (j & 1) ? 0x7632 : 0x5410), s, lo);
       const uint32_t a = vw[j >> 1][0] >> (16 * (j & 1)), b = vw[j >> 1][1] >> (16 * (j & 1));
       wv.x = value2<kF16>(a & 15, (a >> 4) & 15, s, lo);
       wv.y = value2<kF16>((a >> 8) & 15, (a >> 12) & 15, s, lo);

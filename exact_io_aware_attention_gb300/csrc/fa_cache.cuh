@@ -7,8 +7,8 @@
 //
 //   offset 0      K codes   16 rows of d/2 bytes
 //          8 d    V codes   8 rows of d bytes, for pairs of tokens
-//          16 d   K groups  16 rows of d/32 words: s (low half), lo (high half)
-//          18 d   V groups  likewise
+//          16 d   K groups  16 rows of d/32 lo, d/32 s
+//          18 d   V groups  s, then lo: 8 rows of d/32 words, for pairs of tokens
 //
 // Within a cell the order of rows and nibbles is that of the registers of the
 // 16x8x16 matrix product the attention kernel runs on a cell, so a thread
@@ -16,8 +16,8 @@
 // a word into two f16 operands: 4 bits in the low mantissa bits of an f16 are
 // the subnormal u * 2^-24 (u * 2^-20 one nibble up), exact in the product.
 //
-//   token j of a cell is matrix row cell_slot(j); K codes and both group
-//   arrays are in slot order;
+//   token j of a cell is matrix row cell_slot(j); K codes and groups are in
+//   slot order;
 //   K: channel c = 32 g + 8 t + i is nibble i of word (t, g); channels i and
 //   i + 4, in the two halves, are k-neighbours of the product;
 //   V: channel c = 32 g + 4 r + i of tokens t + 8 y and t + 8 y + 4, which are
@@ -73,14 +73,25 @@ __host__ __device__ constexpr int v_half(int j, int r, int g) {
   return v_word<D>(j >> 3, j & 3, r, g) + ((j >> 2) & 1) * 2;
 }
 
-// Byte offset of the group word (s, lo) of a slot.
+// Byte offsets of the 16-bit s and lo of K's group (slot, g): a row holds the
+// lo of its groups, then their s, so that two groups' lo are a word.
 template <int D>
-__host__ __device__ constexpr int k_group(int slot, int g) {
-  return cell_k_groups(D) + slot * (D / 8) + g * 4;
+__host__ __device__ constexpr int k_lo(int slot, int g) {
+  return cell_k_groups(D) + slot * (D / 8) + g * 2;
 }
 template <int D>
-__host__ __device__ constexpr int v_group(int slot, int g) {
-  return cell_v_groups(D) + slot * (D / 8) + g * 4;
+__host__ __device__ constexpr int k_s(int slot, int g) {
+  return k_lo<D>(slot, g) + D / 16;
+}
+// Byte offsets of V's words (y, t, g) of s and of lo: tokens t + 8 y (low half)
+// and t + 8 y + 4.
+template <int D>
+__host__ __device__ constexpr int v_s(int y, int t, int g) {
+  return cell_v_groups(D) + ((4 * y + t) * (D / 32) + g) * 4;
+}
+template <int D>
+__host__ __device__ constexpr int v_lo(int y, int t, int g) {
+  return v_s<D>(y, t, g) + D;
 }
 
 // The pool and the page table of a call. Cell c of sequence b and head h (its
@@ -148,15 +159,9 @@ constexpr int cache_forward_row_tiles(int d, long long rows) {
   return d == 256 || rows <= 8 ? 1 : 2;
 }
 // Whether sequences of at most `tokens` tokens are not split between CTAs.
-#ifndef FA_WHOLE
-#define FA_WHOLE 1024
-#endif
-constexpr bool cache_forward_whole(long long tokens) { return tokens <= FA_WHOLE; }
+constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 // CTAs of the attention kernel that one SM holds (its registers allow).
 constexpr int cache_forward_ctas_per_sm(int d, int row_tiles) {
-#ifdef FA_C128
-  if (row_tiles == 1 && d == 128) return FA_C128;
-#endif
   return row_tiles == 1 ? (d == 256 ? 2 : d == 128 ? 3 : 4) : (d == 64 ? 3 : 2);
 }
 
