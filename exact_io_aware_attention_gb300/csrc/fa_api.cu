@@ -557,6 +557,7 @@ fa_status cache_pool(const fa_cache *c, const int32_t *table, int64_t table_stri
   out->num_pages = c->num_pages;
   out->heads = c->heads;
   out->page_cells = c->page_size / fa::kCellTokens;
+  out->by_page_cells = fa::FastDiv(out->page_cells);
   out->table_cells = max_pages * out->page_cells;
   out->d = c->d;
   out->f16 = c->dtype == FA_F16 ? 1 : 0;
@@ -663,6 +664,7 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
   p.B = B;
   p.hq = Hq;
   p.group = Hq / cache->heads;
+  p.by_group = fa::FastDiv(p.group);
   p.nq = Nq;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)

@@ -65,7 +65,7 @@ __device__ __forceinline__ CellTask find(const CacheRowsParams &p, uint32_t x, u
     atomicCAS(p.status, 0u, index_code(kernel, 1));
     return task;
   }
-  const int pi = (int)c / p.pool.page_cells;
+  const int pi = p.pool.by_page_cells.div((int)c);
   const int page = p.pool.table[(size_t)((long long)task.b * p.pool.table_stride + pi)];
   if (!p.pool.page_ok(page)) {
     atomicCAS(p.status, 0u, index_code(kernel, 2));

@@ -94,6 +94,23 @@ __host__ __device__ constexpr int v_lo(int y, int t, int g) {
   return v_s<D>(y, t, g) + D;
 }
 
+// Division of 0 <= x < 2^31 by a number known at the launch (d >= 1), as a
+// product: mul = ceil(2^(31 + shift) / d) with 2^shift >= d exceeds the
+// quotient 2^(31 + shift) / d by less than 1, which x / 2^31 < 1 of turns into
+// less than the distance of x / d from the next whole number, 1 / d.
+struct FastDiv {
+  uint32_t mul;
+  int shift, d;
+  FastDiv() = default;
+  __host__ explicit FastDiv(int by) : mul(0), shift(0), d(by) {
+    while ((1ll << shift) < by) ++shift;
+    mul = (uint32_t)((((1ull << 31) << shift) + by - 1) / by);
+  }
+  __host__ __device__ __forceinline__ int div(int x) const {
+    return (int)(((uint64_t)(uint32_t)x * mul) >> (31 + shift));
+  }
+};
+
 // The pool and the page table of a call. Cell c of sequence b and head h (its
 // tokens 16 c .. 16 c + 15) is cell_ptr(page, h, c % page_cells), page =
 // table[b * table_stride + c / page_cells].
@@ -104,6 +121,7 @@ struct CachePool {
   int num_pages, heads, page_cells;   // page_cells = page_size / 16
   int table_cells;                    // cells a row of the table covers
   int d, f16;
+  FastDiv by_page_cells;
   __device__ __forceinline__ bool page_ok(int page) const {
     return (unsigned)page < (unsigned)num_pages;
   }
@@ -136,6 +154,7 @@ struct CacheFwdParams {
   float *lse;                         // [B][Hq][nq]
   int o_f32;
   int B, hq, group, nq, causal;       // group = hq / heads of the pool
+  FastDiv by_group, by_row_blocks;    // (row blocks: of the chosen row tiles)
   float scale_log2;
   float *part;                        // scratch: [ctas][2][rows][d] partial outputs,
   float *part_lse;                    // [ctas][2][rows] their log2-sum-exp,

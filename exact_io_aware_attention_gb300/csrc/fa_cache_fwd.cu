@@ -155,7 +155,7 @@ struct Blocks {
   // New tokens, length and visible keys of block x. A length or count out of
   // range is clamped (and recorded by `note`).
   __device__ __forceinline__ void shape(int x, int &n, int &len, int &vis, bool note) const {
-    const int b = x / row_blocks, rb = x - b * row_blocks;
+    const int b = p.by_row_blocks.div(x), rb = x - b * row_blocks;
     len = p.lengths[b];
     n = p.counts ? p.counts[b] : p.nq;
     const int cap = p.pool.table_cells * kCellTokens;
@@ -163,8 +163,8 @@ struct Blocks {
       atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 3));
     len = min(max(len, 0), cap);
     n = min(max(n, 0), p.nq);
-    const int first = rb * rows / p.group;  // first new token of the block
-    const int last = min((rb * rows + rows - 1) / p.group, n - 1);
+    const int first = p.by_group.div(rb * rows);  // first new token of the block
+    const int last = min(p.by_group.div(rb * rows + rows - 1), n - 1);
     vis = first >= n ? 0 : p.causal ? min(len, max(len - n + last + 1, 0)) : len;
   }
   // Its segments' weight on the work axis: their units, or one for a segment
@@ -248,7 +248,9 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       if (x0 > 0) __syncthreads();  // misc[4..7] have been read
       scan(x0, blockIdx.x == 0);
     }
-    share = max((total + gridDim.x - 1) / gridDim.x, (long long)(p.whole ? 1 : kMinShare));
+    share = total < (1ll << 31) ? (long long)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+                                : (total + gridDim.x - 1) / gridDim.x;
+    share = max(share, (long long)(p.whole ? 1 : kMinShare));
     f = share * blockIdx.x;
     f_end = min(f + share, total);
     if (n_blocks <= kThreads) {
@@ -274,57 +276,72 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     const int blk = misc[8], n = misc[9], len = misc[10], vis = misc[11];
     const long long blk_at = *reinterpret_cast<long long *>(misc + 12);
     const int tiles = blocks.tiles(vis), weight = blocks.weight(vis);
-    const int h = int((f - blk_at) / weight);
+    const long long into = f - blk_at;
+    const int h = into < (1ll << 31) ? int((uint32_t)into / (uint32_t)weight) : int(into / weight);
     if (h < 0 || h >= heads) break;
     const long long seg_at = blk_at + (long long)h * weight;
     const int t0 = int(f - seg_at);
     const int t1 = p.whole ? tiles : int(min((long long)tiles, f_end - seg_at));
-    const int b = blk / blocks.row_blocks, row0 = (blk - b * blocks.row_blocks) * kRows;
+    const int b = p.by_row_blocks.div(blk), row0 = (blk - b * blocks.row_blocks) * kRows;
     const int cells = (vis + kCellTokens - 1) / kCellTokens;
     // this warp's pairs of cells: cells 2 (p0 + 4 k) and the next, k < nk
     const int p0 = t0 * kWarps + warp;
     const int p_end = min(t1 * kWarps, (cells + 1) / 2);
     const int nk = p0 < p_end ? (p_end - p0 + kWarps - 1) / kWarps : 0;
 
+    // This thread's part of the query rows, on its way while the cells are
+    // looked up: row r of each n-tile, channels 8 t .. 8 t + 7 of every group.
+    uint4 w[NT][kG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + nt * 8 + r;
+      const int tok = p.by_group.div(row), hq = h * p.group + (row - tok * p.group);
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        w[nt][g] = make_uint4(0, 0, 0, 0);
+        if (tok < n)
+          w[nt][g] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                      p.sq.row(b, hq, tok) + g * 32 + t * 8);
+      }
+    }
+
     // Places of pair k's cells, as cell numbers of the pool: lane k % 32 looks
-    // up those of 32 pairs at a time, one batch ahead. A page holds an even
+    // up those of 32 pairs at a time, a batch ahead. A page holds an even
     // number of cells, and the pair is one copy, or the two are found apart.
     const int32_t *const table = p.pool.table + (size_t)((long long)b * p.pool.table_stride);
     const bool apart = p.pool.page_cells & 1;
     constexpr uint32_t kNoCell = 0xffffffffu;
     bool bad_page = false;  // some page of this piece was not found
-    auto place = [&](int c) {
-      if (c >= cells) return kNoCell;
-      const int pi = c / p.pool.page_cells;
-      const int page = table[pi];
+    int page0 = 0, page1 = 0;  // pages of the batch ahead
+    uint32_t at0 = kNoCell, at1 = kNoCell;
+    auto look_up = [&](int k) {
+      const int c = 2 * (p0 + kWarps * (k + lane));
+      if (k + lane < nk) page0 = table[p.pool.by_page_cells.div(c)];
+      if (apart && k + lane < nk && c + 1 < cells) page1 = table[p.pool.by_page_cells.div(c + 1)];
+    };
+    auto place = [&](int page, int c) {
       if (!p.pool.page_ok(page)) {
         bad_page = true;
         atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
         return kNoCell;
       }
-      return ((uint32_t)page * heads + h) * p.pool.page_cells + (c - pi * p.pool.page_cells);
+      return ((uint32_t)page * heads + h) * p.pool.page_cells +
+             (c - p.pool.by_page_cells.div(c) * p.pool.page_cells);
     };
-    uint32_t at0 = kNoCell, at1 = kNoCell, next0 = kNoCell, next1 = kNoCell;
-    auto look_up = [&](int k) {
-      next0 = next1 = kNoCell;
-      if (k + lane < nk) {
-        const int c = 2 * (p0 + kWarps * (k + lane));
-        next0 = place(c);
-        if (apart) next1 = place(c + 1);
-      }
+    auto take_over = [&](int k) {  // the batch ahead, of pairs k + lane
+      const int c = 2 * (p0 + kWarps * (k + lane));
+      at0 = k + lane < nk ? place(page0, c) : kNoCell;
+      at1 = apart && k + lane < nk && c + 1 < cells ? place(page1, c + 1) : kNoCell;
       bad_page = __any_sync(0xffffffffu, bad_page);
     };
     look_up(0);
-    at0 = next0;
-    at1 = next1;
-    if (nk > 32) look_up(32);
+    take_over(0);
     int issued = 0;
     uint32_t issue_stage = stage;
     auto issue = [&]() {
       const int k = issued;
       if ((k & 31) == 0 && k > 0) {
-        at0 = next0;
-        at1 = next1;
+        take_over(k);
         look_up(k + 32);
       }
       const uint32_t c0 = __shfl_sync(0xffffffffu, at0, k & 31);
@@ -342,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       ++issued;
     };
     while (issued < min(nk, kNs)) issue();
+    look_up(32);
 
     // ---- Q as the B operand of S^T -----------------------------------------
-    // Thread (r, t) holds, of query row r of each n-tile, channels 8 t .. 8 t + 7
-    // of every group: pairs (0,4), (1,5) for the group's first 16-deep product,
-    // (2,6), (3,7) for the second; the pairs that meet nibbles 1 and 3 of a
+    // Of a group's 8 channels: pairs (0,4), (1,5) for the group's first 16-deep
+    // product, (2,6), (3,7) for the second; the pairs that meet nibbles 1 and 3 of a
     // half word (codes * 2^-20) are scaled by 2^-4. qs: the sums of q over the
     // groups as the B operand of the product with lo, whose 16 columns are the
     // groups (two, four or eight) repeated, with one term of a sum each.
@@ -358,23 +375,15 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
     int lim[NT][2];          // visible keys of the row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + r;
-      const int tok = row / p.group, hq = h * p.group + (row - tok * p.group);
-      const bool live = tok < n;
-      uint4 w[kG];
       float big = 0.f;
       bool finite = true;
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        w[g] = make_uint4(0, 0, 0, 0);
-        if (live)
-          w[g] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                  p.sq.row(b, hq, tok) + g * 32 + t * 8);
         float x[8];
-        unpack2<kF16>(w[g].x, x[0], x[1]);
-        unpack2<kF16>(w[g].y, x[2], x[3]);
-        unpack2<kF16>(w[g].z, x[4], x[5]);
-        unpack2<kF16>(w[g].w, x[6], x[7]);
+        unpack2<kF16>(w[nt][g].x, x[0], x[1]);
+        unpack2<kF16>(w[nt][g].y, x[2], x[3]);
+        unpack2<kF16>(w[nt][g].z, x[4], x[5]);
+        unpack2<kF16>(w[nt][g].w, x[6], x[7]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           big = fmaxf(big, fabsf(x[i]));
@@ -393,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         float q8[8];
-        unpack2<kF16>(w[g].x, q8[0], q8[1]);
-        unpack2<kF16>(w[g].y, q8[2], q8[3]);
-        unpack2<kF16>(w[g].z, q8[4], q8[5]);
-        unpack2<kF16>(w[g].w, q8[6], q8[7]);
+        unpack2<kF16>(w[nt][g].x, q8[0], q8[1]);
+        unpack2<kF16>(w[nt][g].y, q8[2], q8[3]);
+        unpack2<kF16>(w[nt][g].z, q8[4], q8[5]);
+        unpack2<kF16>(w[nt][g].w, q8[6], q8[7]);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const float a = finite ? q8[x] * up : 0.f, c = finite ? q8[x + 4] * up : 0.f;
@@ -434,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4) * p.scale_log2 * 0x1p24f;
-        const int tk = (row0 + nt * 8 + 2 * t + y) / p.group;
+        const int tk = p.by_group.div(row0 + nt * 8 + 2 * t + y);
         lim[nt][y] = p.causal && tk < n ? len - n + tk + 1 : len;
       }
     }
     // keys before `all` are visible to every row (rows behind the last new
     // token see what they like and are written as zeros)
-    const int all = p.causal ? min(vis, len - n + row0 / p.group + 1) : vis;
+    const int all = p.causal ? min(vis, len - n + p.by_group.div(row0) + 1) : vis;
 
     float acc[kG][2][NT][4];  // O^T: channels 32 g + 4 r + 2 half + {0 (c0, c1), 1 (c2, c3)}
     // bf16: row g (c0, c1 of the threads r = g): sum of p lo of group g.
@@ -572,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         if constexpr (kMasked) {
           const int cc = c + x2;
           const bool there =
-              cc < cells && !(bad_page && !p.pool.page_ok(table[cc / p.pool.page_cells]));
+              cc < cells && !(bad_page && !p.pool.page_ok(table[p.pool.by_page_cells.div(cc)]));
           // rows behind the sequence may hold anything: s = lo = 0 keeps it out
           const int end = end_of[x2] = there ? vis : 0;
           const int ka = cc * kCellTokens + cell_token(r), kb = ka + 8;
@@ -881,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         o.z = fmaf(wt, a.z, o.z);
         o.w = fmaf(wt, a.w, o.w);
       }
-      const int tok = (row0 + row) / p.group, hq = h * p.group + (row0 + row - tok * p.group);
+      const int tok = p.by_group.div(row0 + row), hq = h * p.group + (row0 + row - tok * p.group);
       const bool none = ll == 0.f || tok >= n;  // sees no key, or is no token
       const float inv = 1.f / ll;
       o = none ? make_float4(0.f, 0.f, 0.f, 0.f)
@@ -946,8 +955,8 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int4 c = p.chain[x];
   if (c.x < 0) return;
   const int row_blocks = (p.nq * p.group + kRows - 1) / kRows;
-  const int b = c.x / row_blocks, row0 = (c.x - b * row_blocks) * kRows;
-  const int tok = (row0 + row) / p.group, hq = c.y * p.group + (row0 + row - tok * p.group);
+  const int b = p.by_row_blocks.div(c.x), row0 = (c.x - b * row_blocks) * kRows;
+  const int tok = p.by_group.div(row0 + row), hq = c.y * p.group + (row0 + row - tok * p.group);
   if (tok >= p.nq) return;
   // the first later CTA in which the segment ends
   if (threadIdx.x == 0) s_last = p.ctas - 1;
@@ -1065,6 +1074,7 @@ template <int D, int NT>
 cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
   // no more CTAs than units that sequences as long as the table could have
   CacheFwdParams p = all;
+  p.by_row_blocks = FastDiv((p.nq * p.group + 8 * NT - 1) / (8 * NT));
   const double segments =
       (double)p.B * ((p.nq * p.group + 8 * NT - 1) / (8 * NT)) * p.pool.heads;
   const double shares =
