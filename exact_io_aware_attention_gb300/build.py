@@ -21,8 +21,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_d256.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_bwd_d256.cu",
-           "fa_bwd_fused.cu", "fa_bwd_fused_q64.cu", "fa_cache.cu", "fa_cache_fwd.cu"]
-HEADERS = ["ptx.cuh", "fa_internal.h", "tile_store.cuh", "fa_cache.cuh"]
+           "fa_bwd_fused.cu", "fa_bwd_fused_q64.cu", "fa_cache.cu", "fa_cache_fwd.cu",
+           "fa_cache_fwd_tc.cu"]
+HEADERS = ["ptx.cuh", "fa_internal.h", "tile_store.cuh", "fa_cache.cuh", "fa_cache_work.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -605,9 +605,9 @@ struct CacheScratch {
 };
 bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, long long tokens, CacheScratch *out) {
   if (sms <= 0 || Hk <= 0) return false;
-  const int nt = fa::cache_forward_row_tiles(d, (long long)(Hq / Hk) * Nq);
-  out->ctas = sms * fa::cache_forward_ctas_per_sm(d, nt);
-  const size_t rows = (size_t)out->ctas * 2 * 8 * nt;
+  const int block_rows = fa::cache_forward_block_rows(d, (long long)(Hq / Hk) * Nq);
+  out->ctas = sms * fa::cache_forward_ctas_per_sm(d, block_rows);
+  const size_t rows = (size_t)out->ctas * 2 * block_rows;
   out->part = round_up(rows * d * sizeof(float));
   out->lse = round_up(rows * sizeof(float));
   out->chain = round_up((size_t)out->ctas * sizeof(int4));
@@ -795,6 +795,7 @@ const char *fa_kernel_name(int kind) {
     case fa::kKindCacheRead: return "fa_cache_read";
     case fa::kKindCacheFwd: return "fa_cache_fwd";
     case fa::kKindCacheCombine: return "fa_cache_combine";
+    case fa::kKindCacheFwdTc: return "fa_cache_fwd_tc";
     default: return "";
   }
 }

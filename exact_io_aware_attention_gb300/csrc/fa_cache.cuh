@@ -170,18 +170,24 @@ cudaError_t launch_cache_write(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream);
 
-// Query rows (new tokens times query heads of one K/V head) that one CTA of
-// the attention kernel holds, in tiles of 8, the columns of its product: one
-// tile where that holds them all, else two (one for d = 256, whose outputs
-// would not fit the registers).
-constexpr int cache_forward_row_tiles(int d, long long rows) {
-  return d == 256 || rows <= 8 ? 1 : 2;
+// The attention with 128 query rows a CTA on tcgen05 (fa_cache_fwd_tc.cu), d up
+// to 128; the merge of its parts is launched by launch_cache_forward.
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream);
+
+// Query rows (new tokens times query heads of one K/V head) that one CTA
+// holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
+// tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 in
+// the one for many.
+constexpr int cache_forward_block_rows(int d, long long rows) {
+  return d == 256 || rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
 }
-// Whether sequences of at most `tokens` tokens are not split between CTAs.
-constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
-// CTAs of the attention kernel that one SM holds (its registers allow).
-constexpr int cache_forward_ctas_per_sm(int d, int row_tiles) {
-  return row_tiles == 1 ? (d == 256 ? 2 : d == 128 ? 3 : 4) : (d == 64 ? 3 : 2);
+// CTAs that one SM holds (its registers and shared memory allow).
+constexpr int cache_forward_ctas_per_sm(int d, int block_rows) {
+  return block_rows == 128 ? 1
+         : block_rows == 8 ? (d == 256 ? 2 : d == 128 ? 3 : 4)
+                           : (d == 64 ? 3 : 2);
 }
 
+// Whether sequences of at most `tokens` tokens are not split between CTAs.
+constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 }  // namespace fa

@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "fa_cache.cuh"
+#include "fa_cache_work.cuh"
 #include "ptx.cuh"
 
 namespace fa {
@@ -56,11 +57,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnitTokens = 2 * kWarps * kCellTokens;  // a pair of cells for each warp
-constexpr int kMinShare = 2;       // units of a CTA at least
+static_assert(kUnitTokens == 2 * kWarps * kCellTokens, "a pair of cells for each warp");
 constexpr float kNoMax = -3e38f;   // m before the first visible key
 constexpr float kMid = 7.5f;       // the middle of the codes
-constexpr float kLn2 = 0.69314718055994531f;
 // m keeps p s below kMaxWeight, and p below kMaxWeight / kSmallStep unless V
 // is as small as that; |v| counts from 2^-90 (p and its sum stay finite).
 constexpr float kMaxWeight = 256.f, kSmallStep = 0x1p-32f;
@@ -69,7 +68,7 @@ constexpr float kMinSize = 0x1p-90f, kMaxSize = 0x1p100f;
 // Ring of a warp: pairs of cells in flight, what the SM's shared memory holds
 // for its CTAs: 150-200 KB an SM, the bytes in flight that HBM's latency needs.
 template <int D, int NT>
-constexpr int kStages = (220 * 1024 / cache_forward_ctas_per_sm(D, NT) - 2048) /
+constexpr int kStages = (220 * 1024 / cache_forward_ctas_per_sm(D, 8 * NT) - 2048) /
                         (kWarps * 2 * cell_bytes(D));
 
 template <int D, int NT>
@@ -82,7 +81,7 @@ struct Layout {
   static constexpr int kBars = kWarps * kWarp;                       // [warp][stage] mbarriers
   static constexpr int kStat = kBars + (kWarps * kNs * 8 + 15) / 16 * 16;  // [warp][8 NT] m, then l
   static constexpr int kMisc = kStat + 2 * kWarps * 8 * NT * 4;      // scan and flags
-  static constexpr int kBytes = kMisc + 128;
+  static constexpr int kBytes = kMisc + kWorkBytes;
   static_assert(kNs >= 2 && kBars % 8 == 0 && kMisc % 16 == 0, "ring and alignment");
 };
 
@@ -116,68 +115,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void lds64(uint32_t a, uint32_t &x, uint32_t &y) {
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void lds128(uint32_t a, uint32_t &x, uint32_t &y, uint32_t &z,
-                                       uint32_t &w) {
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
-               : "r"(a)
-               : "memory");
-}
-// kN consecutive words; the address is aligned to the widest load that fits.
-template <int kN>
-__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *w) {
-  if constexpr (kN == 2) {
-    lds64(a, w[0], w[1]);
-  } else if constexpr (kN == 3) {
-    w[0] = lds32(a);
-    w[1] = lds32(a + 4);
-    w[2] = lds32(a + 8);
-  } else {
-    lds128(a, w[0], w[1], w[2], w[3]);
-    if constexpr (kN == 8) lds128(a + 16, w[4], w[5], w[6], w[7]);
-  }
-}
-
-// Query blocks on the work axis: block x = (sequence b, row block rb) has
-// `heads` segments of tiles(x) units each.
-struct Blocks {
-  const CacheFwdParams &p;
-  int row_blocks, rows;  // rows: query rows of a block
-
-  // New tokens, length and visible keys of block x. A length or count out of
-  // range is clamped (and recorded by `note`).
-  __device__ __forceinline__ void shape(int x, int &n, int &len, int &vis, bool note) const {
-    const int b = p.by_row_blocks.div(x), rb = x - b * row_blocks;
-    len = p.lengths[b];
-    n = p.counts ? p.counts[b] : p.nq;
-    const int cap = p.pool.table_cells * kCellTokens;
-    if (note && (len < 0 || len > cap || n < 0 || n > p.nq))
-      atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 3));
-    len = min(max(len, 0), cap);
-    n = min(max(n, 0), p.nq);
-    const int first = p.by_group.div(rb * rows);  // first new token of the block
-    const int last = min(p.by_group.div(rb * rows + rows - 1), n - 1);
-    vis = first >= n ? 0 : p.causal ? min(len, max(len - n + last + 1, 0)) : len;
-  }
-  // Its segments' weight on the work axis: their units, or one for a segment
-  // that stays whole.
-  __device__ __forceinline__ int weight(int vis) const { return p.whole ? 1 : tiles(vis); }
-  // A segment without visible keys has one unit too: its rows are written.
-  __device__ __forceinline__ int tiles(int vis) const {
-    return max(1, (vis + kUnitTokens - 1) / kUnitTokens);
-  }
-};
-
 template <int D, int NT, bool kF16>
-__global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
+__global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT))
     fa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using L = Layout<D, NT>;
   constexpr int kG = D / 32, kNs = L::kNs, kRows = 8 * NT, kF = 1;
@@ -189,8 +128,6 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
   const uint32_t ring = sbase + warp * L::kWarp;
   const uint32_t bars = sbase + L::kBars + warp * kNs * 8;
   float *const stat = reinterpret_cast<float *>(smem + L::kStat);
-  // [0] abort, [4..7] scan, [8..13] the block of the next piece: number, new
-  // tokens, length, visible keys, begin (64 bits)
   int *const misc = reinterpret_cast<int *>(smem + L::kMisc);
   const StatusSlot st = {p.status, misc, p.wait_limit_ns};
 
@@ -202,88 +139,21 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
   fence_mbar_init();
 
   const Blocks blocks{p, (p.nq * p.group + kRows - 1) / kRows, kRows};
-  const int n_blocks = p.B * blocks.row_blocks, heads = p.pool.heads;
+  const int heads = p.pool.heads;
 
-  // This CTA's share [f, f_end) of the axis: the total, then the block in
-  // which f lies, by block-wide scans over the blocks' sizes (one scan where
-  // the threads hold all blocks). Everything that decides which piece comes
-  // next is read once and handed to all threads through shared memory: they
-  // agree even on values that change under the kernel.
-  long long total = 0, share, f, f_end;
-  bool found = false;
-  {
-    int x = threadIdx.x, n = 0, len = 0, vis = 0, size = 0;
-    long long at = 0;  // where block x begins
-    auto scan = [&](int x0, bool note) {
-      x = x0 + threadIdx.x;
-      size = 0;
-      if (x < n_blocks) {
-        blocks.shape(x, n, len, vis, note);
-        size = blocks.weight(vis);
-      }
-      int incl = size;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) misc[4 + warp] = incl;
-      __syncthreads();
-      int before = 0;
-      for (int w = 0; w < warp; ++w) before += misc[4 + w];
-      at = total + (long long)(before + incl - size) * heads;
-      total += (long long)(misc[4] + misc[5] + misc[6] + misc[7]) * heads;
-    };
-    auto find = [&] {
-      if (size > 0 && f >= at && f < at + (long long)size * heads) {
-        misc[8] = x;
-        misc[9] = n;
-        misc[10] = len;
-        misc[11] = vis;
-        *reinterpret_cast<long long *>(misc + 12) = at;
-      }
-      __syncthreads();
-    };
-    for (int x0 = 0; x0 < n_blocks; x0 += kThreads) {
-      if (x0 > 0) __syncthreads();  // misc[4..7] have been read
-      scan(x0, blockIdx.x == 0);
-    }
-    share = total < (1ll << 31) ? (long long)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
-                                : (total + gridDim.x - 1) / gridDim.x;
-    share = max(share, (long long)(p.whole ? 1 : kMinShare));
-    f = share * blockIdx.x;
-    f_end = min(f + share, total);
-    if (n_blocks <= kThreads) {
-      found = f < f_end;
-      find();
-    } else {
-      const long long all = total;
-      total = 0;
-      for (int x0 = 0; x0 < n_blocks && f < all && !found; x0 += kThreads) {
-        __syncthreads();
-        scan(x0, false);
-        find();
-        found = f < total;
-      }
-    }
-  }
+  const Share mine = find_share<kThreads>(p, blocks, misc);
+  long long f = mine.f;
+  const long long f_end = mine.f_end;
   int4 chain = make_int4(-1, 0, 0, 0);
 
   uint32_t stage = 0, phase = 0;  // ring position of the next pair to consume
   bool first_piece = true;
-  while (found && f < f_end) {
+  while (mine.found && f < f_end) {
     // ---- the piece: units [t0, t1) of a segment --------------------------
-    const int blk = misc[8], n = misc[9], len = misc[10], vis = misc[11];
-    const long long blk_at = *reinterpret_cast<long long *>(misc + 12);
-    const int tiles = blocks.tiles(vis), weight = blocks.weight(vis);
-    const long long into = f - blk_at;
-    const int h = into < (1ll << 31) ? int((uint32_t)into / (uint32_t)weight) : int(into / weight);
+    const Piece piece(p, blocks, misc, f, f_end);
+    const int n = piece.n, len = piece.len, vis = piece.vis, h = piece.h, b = piece.b;
+    const int row0 = piece.row0, t0 = piece.t0, t1 = piece.t1, cells = piece.cells;
     if (h < 0 || h >= heads) break;
-    const long long seg_at = blk_at + (long long)h * weight;
-    const int t0 = int(f - seg_at);
-    const int t1 = p.whole ? tiles : int(min((long long)tiles, f_end - seg_at));
-    const int b = p.by_row_blocks.div(blk), row0 = (blk - b * blocks.row_blocks) * kRows;
-    const int cells = (vis + kCellTokens - 1) / kCellTokens;
     // this warp's pairs of cells: cells 2 (p0 + 4 k) and the next, k < nk
     const int p0 = t0 * kWarps + warp;
     const int p_end = min(t1 * kWarps, (cells + 1) / 2);
@@ -870,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
       return;
     }
 
-    const bool whole = t0 == 0 && t1 == tiles;
+    const bool whole = t0 == 0 && t1 == piece.tiles;
     const int slot = first_piece ? 0 : 1;
     constexpr int kChunks = D / 4;  // 4 columns a thread
     for (int x = threadIdx.x; x < kRows * kChunks; x += kThreads) {
@@ -910,26 +780,10 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
         if (col == 0) p.lse[((size_t)b * p.hq + hq) * p.nq + tok] = lse2 * kLn2;
       }
     }
-    // chain: the segment that begins here and ends in a later CTA (x: block,
-    // y: head, z: its slot here), and w: whether the segment that an earlier
-    // CTA began and that continues here ends here (1) or goes on (0)
-    if (t0 == 0 && t1 < tiles) chain = make_int4(blk, h, slot, chain.w);
-    if (first_piece && t0 > 0) chain.w = t1 == tiles;
+    piece.link(chain, first_piece);
     first_piece = false;
-
-    f = seg_at + (p.whole ? 1 : t1);
-    if (t1 == tiles && h == heads - 1) {
-      if (blk + 1 == n_blocks) break;
-      if (threadIdx.x == 0) {
-        int n2, len2, vis2;
-        blocks.shape(blk + 1, n2, len2, vis2, false);
-        misc[8] = blk + 1;
-        misc[9] = n2;
-        misc[10] = len2;
-        misc[11] = vis2;
-        *reinterpret_cast<long long *>(misc + 12) = f;
-      }
-    }
+    f = piece.next(p);
+    if (!piece.advance(p, blocks, misc, f)) break;
     fence_proxy_async_smem();  // the next piece's copies overwrite the merge's reads and writes
     __syncthreads();
   }
@@ -943,10 +797,10 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, NT))
 // kSub-th, so that a chain over the whole GPU is a few loads deep.
 constexpr int kCombineThreads = 256;
 
-template <int D, int NT, bool kF16>
+template <int D, int kRows, bool kF16>
 __global__ void __launch_bounds__(kCombineThreads)
     fa_cache_combine_kernel(const __grid_constant__ CacheFwdParams p) {
-  constexpr int kRows = 8 * NT, kChunks = D / 4, kSub = kCombineThreads / kChunks;
+  constexpr int kChunks = D / 4, kSub = kCombineThreads / kChunks;
   __shared__ float4 s_o[kSub][kChunks];
   __shared__ float s_top[kSub], s_sum[kSub];
   __shared__ int s_last;
@@ -1037,29 +891,13 @@ __global__ void __launch_bounds__(kCombineThreads)
         sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
 }
 
-template <int D, int NT, bool kF16>
-cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
-  static std::atomic<bool> configured[64];  // per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(fa_cache_fwd_kernel<D, NT, kF16>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, NT>::kBytes);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) configured[dev].store(true, std::memory_order_release);
-  }
-  {
-    LaunchProbe probe(kKindCacheFwd, stream);
-    fa_cache_fwd_kernel<D, NT, kF16><<<p.ctas, kThreads, Layout<D, NT>::kBytes, stream>>>(p);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess || p.whole) return e;
+template <int D, int kRows, bool kF16>
+cudaError_t launch_combine(const CacheFwdParams &p, cudaStream_t stream) {
   // set up while the attention kernel runs (programmatic dependent launch)
   LaunchProbe probe(kKindCacheCombine, stream);
   const long long rows = (long long)p.nq * p.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < 8 * NT ? rows : 8 * NT));
+  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < kRows ? rows : kRows));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -1067,33 +905,57 @@ cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_cache_combine_kernel<D, NT, kF16>, p);
+  return cudaLaunchKernelEx(&cfg, fa_cache_combine_kernel<D, kRows, kF16>, p);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kF16>
+cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
+  static std::atomic<bool> configured[64];  // per device
+  cudaError_t e = allow_shared_memory(fa_cache_fwd_kernel<D, NT, kF16>, Layout<D, NT>::kBytes,
+                                      configured);
+  if (e != cudaSuccess) return e;
+  LaunchProbe probe(kKindCacheFwd, stream);
+  fa_cache_fwd_kernel<D, NT, kF16><<<p.ctas, kThreads, Layout<D, NT>::kBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kF16>
 cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
-  // no more CTAs than units that sequences as long as the table could have
   CacheFwdParams p = all;
-  p.by_row_blocks = FastDiv((p.nq * p.group + 8 * NT - 1) / (8 * NT));
-  const double segments =
-      (double)p.B * ((p.nq * p.group + 8 * NT - 1) / (8 * NT)) * p.pool.heads;
+  const int rows = cache_forward_block_rows(D, (long long)p.nq * p.group);
+  const int row_blocks = (p.nq * p.group + rows - 1) / rows;
+  p.by_row_blocks = FastDiv(row_blocks);
+  // no more CTAs than shares of sequences as long as the table could have
+  const double segments = (double)p.B * row_blocks * p.pool.heads;
   const double shares =
       p.whole ? segments
               : segments * ((p.pool.table_cells * kCellTokens + kUnitTokens - 1) / kUnitTokens) /
                     kMinShare;
   if (shares < (double)p.ctas) p.ctas = (int)shares + 1;
-  return p.pool.f16 ? launch_d<D, NT, true>(p, stream) : launch_d<D, NT, false>(p, stream);
+  cudaError_t e;
+  if constexpr (D <= 128) {
+    e = rows == 128  ? launch_cache_forward_tc(p, stream)
+        : rows == 16 ? launch_d<D, 2, kF16>(p, stream)
+                     : launch_d<D, 1, kF16>(p, stream);
+    if (e != cudaSuccess || p.whole) return e;
+    return rows == 128  ? launch_combine<D, 128, kF16>(p, stream)
+           : rows == 16 ? launch_combine<D, 16, kF16>(p, stream)
+                        : launch_combine<D, 8, kF16>(p, stream);
+  } else {
+    e = launch_d<D, 1, kF16>(p, stream);
+    return e != cudaSuccess || p.whole ? e : launch_combine<D, 8, kF16>(p, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream) {
-  const bool two = cache_forward_row_tiles(p.pool.d, (long long)p.nq * p.group) == 2;
+  const bool f16 = p.pool.f16 != 0;
   switch (p.pool.d) {
-    case 64: return two ? launch_t<64, 2>(p, stream) : launch_t<64, 1>(p, stream);
-    case 96: return two ? launch_t<96, 2>(p, stream) : launch_t<96, 1>(p, stream);
-    case 128: return two ? launch_t<128, 2>(p, stream) : launch_t<128, 1>(p, stream);
-    case 256: return launch_t<256, 1>(p, stream);
+    case 64: return f16 ? launch_t<64, true>(p, stream) : launch_t<64, false>(p, stream);
+    case 96: return f16 ? launch_t<96, true>(p, stream) : launch_t<96, false>(p, stream);
+    case 128: return f16 ? launch_t<128, true>(p, stream) : launch_t<128, false>(p, stream);
+    case 256: return f16 ? launch_t<256, true>(p, stream) : launch_t<256, false>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

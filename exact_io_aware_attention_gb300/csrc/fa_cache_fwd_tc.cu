@@ -1,0 +1,701 @@
+// Attention over the 4-bit K/V cache for many query rows (a chunk of a prompt,
+// drafted tokens times the query heads of a K/V head): 128 rows a CTA on
+// tcgen05, O = softmax(scale Q K^T) V with K and V expanded in shared memory.
+//
+// With this many rows the products no longer fit the time that the codes take
+// to arrive, so they run on tcgen05, whose operands are 16-bit values: a tile
+// of 128 keys is expanded once for all 128 rows, K^ = lo + s u and V^ likewise,
+// rounded once to f16. What is f16 in bf16 caches too: f16 has three bits more
+// than bf16, and a power of two for each tile (2^eK, 2^eV over its largest
+// |lo|, |lo + 15 s|) takes the place of bf16's exponents: the scores are
+// multiplied with 2^eK in fp32, and the weights P carry 2^eV. The running
+// reference m follows max_j (score_j + eV), so P stays below 2^8 and the
+// accumulators have one scale. Roundings: K^, V^, P 2^-11 relative each (K^ and
+// V^ of elements below 2^-22 of a tile's largest: 2^-25 of 2^-15 of that).
+//
+// The order of the operands is that in which the cache holds its codes, so
+// that they are stored to shared memory as they come out of the words:
+//   K tile   [128 slots][d], K-major: a word's 8 channels are stored in the
+//            order 0 4 1 5 2 6 3 7, and Q's alike;
+//   V^T tile [d][128 slots], K-major: a word holds the two neighbouring slots,
+//            and four words a 16-byte piece of a channel's row;
+//   the columns of S and P are slots (cell_token gives their tokens).
+//
+// CTA: 12 warps, one CTA an SM, pieces of the axis of work as in
+// fa_cache_fwd.cu (the same units, scratch and merge):
+//   warp 0       bulk copies of cells into a ring of two tiles
+//   warp 1       tcgen05 issuer (one lane) and tensor-memory owner
+//   warps 4-7    Q to shared memory, softmax, output (thread = row = TMEM lane)
+//   warps 8-11   expansion of K and V
+// Tensor memory: S_0 [0,128), S_1 [128,256), O [256,256+d), P_0 [384,448),
+// P_1 [448,512). S of the next tile is issued ahead of P V of this one.
+//
+// NaN. A group of V with a non-finite element reads as NaN, but 0 times NaN
+// would spread it to rows that do not see its token. So it enters V^ as 0,
+// and rows that see the token remember the group and put NaN in its channels
+// at the end. A NaN in K needs no such care: hidden scores are overwritten.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cache_work.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128, kKeys = 128, kTileCells = kKeys / kCellTokens;
+constexpr float kRescaleThreshold = 8.0f;  // log2: m moves when P would pass 2^8
+
+template <int D>
+struct TcLayout {
+  static constexpr int kG = D / 32;
+  static constexpr int kChunks = (D + 63) / 64;           // 64-channel chunks of a Q or K row
+  static constexpr int kQkBytes = kChunks * kRows * 128;  // 128 rows of 128 bytes a chunk
+  static constexpr int kVChunk = D * 128;                 // D rows of 64 slots
+  static constexpr int kVBytes = 2 * kVChunk;
+  static constexpr int kPacked = kTileCells * cell_bytes(D);
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kQkBytes;                // two buffers
+  static constexpr int kV = kK + 2 * kQkBytes;            // two buffers
+  static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
+  static constexpr int kMetaK = kRing + 2 * kPacked;      // [slot][g]: (s, s), (lo, lo) in f16
+  static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
+  static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
+  static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][slot] groups of V that are NaN
+  static constexpr int kScales = kNan + 4 * kKeys;        // [4]: 2^eK, 2^eV, 2^-eV, eV
+  static constexpr int kFlags = kScales + 4 * 16;         // [4]: any NaN; [4] found cells; [8] reduction
+  static constexpr int kBars = kFlags + 32 + 48;
+  static constexpr int kNumBars = 18;
+  static constexpr int kTmem = kBars + kNumBars * 8;
+  static constexpr int kMisc = (kTmem + 8 + 15) / 16 * 16;
+  static constexpr int kBytes = kMisc + kWorkBytes;
+  static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 B
+  static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(kBars % 8 == 0 && kRing % 128 == 0 && kV % 1024 == 0, "alignment");
+};
+
+struct TcBars {
+  uint32_t base;
+  __device__ uint32_t packed_full(int s) const { return base + 8 * s; }
+  __device__ uint32_t packed_empty(int s) const { return base + 8 * (2 + s); }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (4 + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (6 + s); }
+  __device__ uint32_t s_full(int s) const { return base + 8 * (8 + s); }   // and K is free
+  __device__ uint32_t s_free(int s) const { return base + 8 * (10 + s); }
+  __device__ uint32_t p_full(int s) const { return base + 8 * (12 + s); }
+  __device__ uint32_t pv_done(int s) const { return base + 8 * (14 + s); }  // and V and P are free
+  __device__ uint32_t q_full() const { return base + 8 * 16; }
+  __device__ uint32_t teardown() const { return base + 8 * 17; }
+};
+
+enum TcRole : uint32_t { kRoleLoad = 1, kRoleMma = 2, kRoleSoftmax = 3, kRoleExpand = 4 };
+constexpr uint32_t code(uint32_t role, uint32_t site) {
+  return status_code(kKernCacheFwdTc, role, site);
+}
+
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  st_shared_v4(a, x, y, z, w);
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)x) : "memory");
+}
+
+// lo + s u of the four pairs of codes of a word (nibble p of either half), with
+// s and lo for the two halves: u is made by joining the bits to 1024 (in the
+// second place 1024 + 16 u), both exact, and the result is rounded once.
+template <int kPair>
+__device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t lo2) {
+  if constexpr (kPair >= 2) w >>= 8;
+  uint32_t u;
+  if constexpr (kPair & 1)
+    u = hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);  // / 16, - 64
+  else
+    u = hadd2((w & 0x000f000fu) | 0x64006400u, 0xe400e400u);               // - 1024
+  return hfma2(u, s2, lo2);
+}
+
+// The barrier of the expansion warps.
+__device__ __forceinline__ void expand_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same, and whether all of them are well: they give up together, since a
+// warp that left alone would leave the others at the barrier.
+__device__ __forceinline__ bool expand_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
+// The power of two at or below x > 0 times 2^-7, between 2^-120 and 2^120 (1 for 0): what
+// brings values up to x below 2^8.
+__device__ __forceinline__ int tile_exponent(float x) {
+  return x > 0.f ? min(max((int)(__float_as_uint(x) >> 23) - 127 - 7, -120), 120) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_cache_fwd_tc_kernel(const __grid_constant__ CacheFwdParams p) {
+  using L = TcLayout<D>;
+  constexpr int kG = L::kG;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *const smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const TcBars bars{sb + L::kBars};
+  int *const misc = reinterpret_cast<int *>(smem + L::kMisc);
+  volatile int *const nan_flag = reinterpret_cast<int *>(smem + L::kFlags);      // [4]
+  volatile int *const found_cells = reinterpret_cast<int *>(smem + L::kFlags) + 4;  // [4] bit masks
+  volatile float *const red = reinterpret_cast<float *>(smem + L::kFlags + 32);  // [3][4]
+  volatile float *const scales = reinterpret_cast<float *>(smem + L::kScales);   // [4][4]
+  const StatusSlot st = {p.status, misc, p.wait_limit_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bars.packed_full(s), 1);
+      mbar_init(bars.packed_empty(s), 128);
+      mbar_init(bars.k_full(s), 128);
+      mbar_init(bars.v_full(s), 128);
+      mbar_init(bars.s_full(s), 1);
+      mbar_init(bars.s_free(s), 128);
+      mbar_init(bars.p_full(s), 128);
+      mbar_init(bars.pv_done(s), 1);
+    }
+    mbar_init(bars.q_full(), 128);
+    mbar_init(bars.teardown(), 1);
+    misc[0] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sb + L::kTmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const Blocks blocks{p, (p.nq * p.group + kRows - 1) / kRows, kRows};
+  const Share mine = find_share<kThreads>(p, blocks, misc);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
+  const int heads = p.pool.heads;
+  int4 chain = make_int4(-1, 0, 0, 0);
+  long long f = mine.f;
+  uint32_t tile0 = 0, pieces = 0;  // tiles and pieces before this one: buffers and parities
+  bool failed = false;
+  while (mine.found && f < mine.f_end) {
+    const Piece piece(p, blocks, misc, f, mine.f_end);
+    if (piece.h < 0 || piece.h >= heads) break;
+    const int n = piece.n, len = piece.len, vis = piece.vis, cells = piece.cells;
+    const int count = max(0, min(piece.t1, (cells + kTileCells - 1) / kTileCells) - piece.t0);
+    // keys before `all` are visible to every row that is a token
+    const int all = p.causal ? min(vis, len - n + p.by_group.div(piece.row0) + 1) : vis;
+
+    if (warp == 0) {
+      // ---- copies ----------------------------------------------------------
+      const int32_t *const table = p.pool.table + (size_t)((long long)piece.b * p.pool.table_stride);
+      const bool one_copy = p.pool.page_cells % kTileCells == 0;
+      auto page_of = [&](int k) {  // of this lane's cell of tile k
+        const int c = (piece.t0 + k) * kTileCells + lane;
+        return lane < kTileCells && k < count && c < cells ? table[p.pool.by_page_cells.div(c)] : -1;
+      };
+      int page = page_of(0);
+      bool ok = true;
+      int issued = 0;
+      for (; issued < count; ++issued) {
+        const uint32_t i = tile0 + issued;
+        const int slot = i & 1;
+        const int ahead = page_of(issued + 1);
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.packed_empty(slot), ((i >> 1) & 1) ^ 1, st,
+                                                   code(kRoleLoad, 1)));
+        if (!ok || (p.debug_flags & kDebugSkipLoads)) break;
+        const int c = (piece.t0 + issued) * kTileCells + lane;
+        const bool wanted = lane < kTileCells && c < cells;
+        const bool here = wanted && p.pool.page_ok(page);
+        if (wanted && !here) atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
+        const uint32_t found = __ballot_sync(0xffffffffu, here);
+        // (one page: all cells of the tile are there, those behind the sequence too)
+        const uint32_t bytes = one_copy ? (found ? (uint32_t)L::kPacked : 0u)
+                                        : __popc(found) * cell_bytes(D);
+        if (lane == 0) {
+          found_cells[i & 3] = (int)found;
+          mbar_arrive_expect_tx(bars.packed_full(slot), bytes);
+        }
+        __syncwarp();
+        if (one_copy ? lane == 0 && found : here)
+          bulk_load_1d(sb + L::kRing + slot * L::kPacked + lane * cell_bytes(D),
+                       p.pool.template cell_ptr<D>(
+                           page, piece.h, c - p.pool.by_page_cells.div(c) * p.pool.page_cells),
+                       one_copy ? bytes : (uint32_t)cell_bytes(D), bars.packed_full(slot));
+        page = ahead;
+      }
+      if (!(p.debug_flags & kDebugSkipLoads))  // every copy issued lands before the piece ends
+        for (int k = max(0, issued - 2); k < issued; ++k)
+          mbar_wait_drain_inl(bars.packed_full((tile0 + k) & 1), ((tile0 + k) >> 1) & 1, st,
+                              code(kRoleLoad, 2));
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---- tcgen05 issuer --------------------------------------------------
+      if (elect_one() && count > 0) {
+        constexpr uint32_t kIdS = idesc_f32acc(kRows, kKeys, 0, 0, true);
+        constexpr uint32_t kIdPV = idesc_f32acc(kRows, D, 0, 0, true);
+        auto issue_s = [&](uint32_t i) {
+          const uint32_t k_base = sb + L::kK + (i & 1) * L::kQkBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
+            mma_f16kind_ss(tmem + (i & 1) * kKeys, sdesc_sw128(sb + L::kQ + off, 16, 1024),
+                           sdesc_sw128(k_base + off, 16, 1024), kIdS, kk > 0);
+          }
+          mma_commit(bars.s_full(i & 1));
+        };
+        bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1)) &&
+                  mbar_wait_inl(bars.k_full(tile0 & 1), (tile0 >> 1) & 1, st, code(kRoleMma, 2));
+        if (ok) {
+          tc_fence_after();
+          issue_s(tile0);
+        }
+        for (int k = 0; k < count && ok; ++k) {
+          const uint32_t i = tile0 + k;
+          if (k + 1 < count) {
+            const uint32_t j = i + 1;
+            ok = mbar_wait_inl(bars.k_full(j & 1), (j >> 1) & 1, st, code(kRoleMma, 3)) &&
+                 mbar_wait_inl(bars.s_free(j & 1), ((j >> 1) & 1) ^ 1, st, code(kRoleMma, 4));
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(j);
+          }
+          ok = mbar_wait_inl(bars.v_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 5)) &&
+               mbar_wait_inl(bars.p_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 6));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_base = sb + L::kV + (i & 1) * L::kVBytes;
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_f16kind_ts(tmem + 256, tmem + 384 + (i & 1) * 64 + kk * 8,
+                           sdesc_sw128(v_base + (kk >> 2) * L::kVChunk + (kk & 3) * 32, 16, 1024),
+                           kIdPV, (k > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bars.pv_done(i & 1));
+        }
+        if (!ok) {  // gave up: what was issued ends before the tensor memory goes
+          mma_commit(bars.teardown());
+          mbar_wait_drain_inl(bars.teardown(), 0, st, code(kRoleMma, 7));
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 8) {
+      // ---- expansion -------------------------------------------------------
+      const int dt = threadIdx.x - 256, dw = warp - 8;
+      bool ok = true;
+      for (int k = 0; k < count; ++k) {
+        const uint32_t i = tile0 + k;
+        const int slot2 = i & 1;
+        const uint32_t parity = (i >> 1) & 1;
+        const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
+        if (!expand_all(ok && mbar_wait_inl(bars.packed_full(slot2), parity, st,
+                                            code(kRoleExpand, 1))))
+          break;
+        const uint32_t found = (uint32_t)found_cells[i & 3];
+        const int key0 = (piece.t0 + k) * kKeys;
+        // s and lo of the token of K slot dt, and of one token of V: this
+        // thread's half z of pair (cell, y, t)
+        float ks[kG], kl[kG], vs[kG], vl[kG];
+        const int cell = dt >> 4, vy = (dt >> 3) & 1, vt = (dt >> 1) & 3, vz = dt & 1;
+        const uint32_t at = ring + cell * cell_bytes(D);
+        const bool there = (found >> cell) & 1;
+        const bool k_live = there && key0 + cell * kCellTokens + cell_token(dt & 15) < vis;
+        const bool v_live = there && key0 + cell * kCellTokens + vt + 8 * vy + 4 * vz < vis;
+        float k_top = 0.f, v_top = 0.f;
+        uint32_t nans = 0;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          float unused;
+          (void)unused;
+          uint16_t h;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + k_s<D>(dt & 15, g)) : "memory");
+          unpack2<kF16>(h, ks[g], unused);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + k_lo<D>(dt & 15, g)) : "memory");
+          unpack2<kF16>(h, kl[g], unused);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + v_s<D>(vy, vt, g) + 2 * vz) : "memory");
+          unpack2<kF16>(h, vs[g], unused);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + v_lo<D>(vy, vt, g) + 2 * vz) : "memory");
+          unpack2<kF16>(h, vl[g], unused);
+          if (!k_live) ks[g] = kl[g] = 0.f;
+          if (!v_live) vs[g] = vl[g] = 0.f;
+          if (!(vl[g] == vl[g])) {
+            nans |= 1u << g;
+            vs[g] = vl[g] = 0.f;
+          }
+          // (a NaN does not enter the maximum)
+          k_top = fmaxf(k_top, fmaxf(fabsf(kl[g]), fabsf(fmaf(15.f, ks[g], kl[g]))));
+          v_top = fmaxf(v_top, fmaxf(fabsf(vl[g]), fabsf(fmaf(15.f, vs[g], vl[g]))));
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          k_top = fmaxf(k_top, __shfl_xor_sync(0xffffffffu, k_top, o));
+          v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
+        }
+        const bool any_nan = __any_sync(0xffffffffu, nans != 0);
+        if (lane == 0) {
+          red[dw] = k_top;
+          red[4 + dw] = v_top;
+          red[8 + dw] = any_nan ? 1.f : 0.f;
+        }
+        expand_sync();  // (and the last tile's groups have been used)
+        const int ek = tile_exponent(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+        const int ev = tile_exponent(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
+        const float fk = pow2(-ek), fv = pow2(-ev);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const float s = ks[g] * fk, lo = kl[g] * fk;
+          sts64(sb + L::kMetaK + (dt * kG + g) * 8, pack_f16x2(s, s), pack_f16x2(lo, lo));
+          const uint32_t o = ((((cell * 2 + vy) * kG + g) * 4 + vt) * 2 + vz) * 2;
+          sts16(sb + L::kMetaV + o, pack_f16x2(vs[g] * fv, 0.f));
+          sts16(sb + L::kVLo + o, pack_f16x2(vl[g] * fv, 0.f));
+        }
+        smem[L::kNan + (i & 3) * kKeys + cell * 16 + cell_slot(vt + 8 * vy + 4 * vz)] = (uint8_t)nans;
+        if (dt == 0) {
+          nan_flag[i & 3] = red[8] + red[9] + red[10] + red[11] > 0.f;
+          scales[(i & 3) * 4] = pow2(ek);
+          scales[(i & 3) * 4 + 1] = pow2(-ev);
+          scales[(i & 3) * 4 + 2] = (float)ev;
+        }
+        expand_sync();
+
+        // K, into the buffer that S of two tiles ago has read
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_inl(bars.s_full(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
+        if (ok) {
+          const uint32_t dst = sb + L::kK + slot2 * L::kQkBytes;
+          const int t = lane & 3, low = (((lane >> 2) & 1) << 2) | (lane >> 3);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int slot = (dw * 4 + x) * 8 + low;
+            uint32_t w[kG];
+            lds_words<kG>(ring + (slot >> 4) * cell_bytes(D) + k_word<D>(slot & 15, t, 0), w);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              uint32_t s2, lo2;
+              lds64(sb + L::kMetaK + (slot * kG + g) * 8, s2, lo2);
+              const int block = (g & 1) * 4 + t;
+              sts128(dst + (g >> 1) * (kRows * 128) + slot * 128 + ((block ^ (slot & 7)) << 4),
+                     expand<0>(w[g], s2, lo2), expand<1>(w[g], s2, lo2), expand<2>(w[g], s2, lo2),
+                     expand<3>(w[g], s2, lo2));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        if (ok) mbar_arrive(bars.k_full(slot2));
+
+        // V, into the buffer that P V of two tiles ago has read
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(slot2), parity ^ 1, st,
+                                                         code(kRoleExpand, 3)));
+        if (ok) {
+          const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
+          // eight lanes that store together: four blocks of 8 slots, two r
+          const int kb = (lane & 3) | (((dw >> 0) & 3) << 2);  // block of 8 slots: cell * 2 + y
+          const int r = lane >> 2;
+          const uint32_t from = ring + (kb >> 1) * cell_bytes(D);
+          uint32_t w[4][kG];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) lds_words<kG>(from + v_word<D>(kb & 1, t, r, 0), w[t]);
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            uint32_t s2[4], lo2[4];
+            lds128(sb + L::kMetaV + (kb * kG + g) * 16, s2[0], s2[1], s2[2], s2[3]);
+            lds128(sb + L::kVLo + (kb * kG + g) * 16, lo2[0], lo2[1], lo2[2], lo2[3]);
+            auto row = [&](auto pair) {  // channel 32 g + 4 r + pair
+              constexpr int kPair = decltype(pair)::value;
+              const int c = 32 * g + 4 * r + kPair;
+              sts128(dst + (kb >> 3) * L::kVChunk + c * 128 + (((kb & 7) ^ (c & 7)) << 4),
+                     expand<kPair>(w[0][g], s2[0], lo2[0]), expand<kPair>(w[1][g], s2[1], lo2[1]),
+                     expand<kPair>(w[2][g], s2[2], lo2[2]), expand<kPair>(w[3][g], s2[3], lo2[3]));
+            };
+            row(std::integral_constant<int, 0>{});
+            row(std::integral_constant<int, 1>{});
+            row(std::integral_constant<int, 2>{});
+            row(std::integral_constant<int, 3>{});
+          }
+        }
+        fence_proxy_async_smem();
+        if (ok) {
+          mbar_arrive(bars.v_full(slot2));
+          mbar_arrive(bars.packed_empty(slot2));
+        }
+      }
+    } else if (warp >= 4) {
+      // ---- Q, softmax, output ------------------------------------------------
+      const int r = threadIdx.x - 128;
+      const int row = piece.row0 + r;
+      const int tok = p.by_group.div(row), hq = piece.h * p.group + (row - tok * p.group);
+      const bool live = tok < n;
+      const bool warp_live = p.by_group.div(piece.row0 + (warp - 4) * 32) < n;  // its first row's token
+      float c_row = 0.f;
+      {
+        // the row scaled by a power of two, its largest element below 2^11
+        const uint16_t *const src = static_cast<const uint16_t *>(p.q) +
+                                    (live ? p.sq.row(piece.b, hq, tok) : (size_t)0);
+        float big = 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (live) w = *reinterpret_cast<const uint4 *>(src + x * 8);
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float a, b;
+            unpack2<kF16>(in[y], a, b);
+            big = fmaxf(big, fmaxf(fabsf(a), fabsf(b)));
+            finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+          }
+        }
+        const int e = max((int)(__float_as_uint(big) >> 23), 40);
+        const bool scaled = big > 0.f && finite;
+        // (a row with an infinity or a NaN is NaN throughout: so are its scores)
+        const float up = !finite ? __uint_as_float(0x7fffffffu)
+                         : scaled ? __uint_as_float((uint32_t)(264 - e) << 23)
+                                  : 1.f;
+        c_row = (scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f) * p.scale_log2;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (live) w = *reinterpret_cast<const uint4 *>(src + x * 8);
+          float q[8];
+          unpack2<kF16>(w.x, q[0], q[1]);
+          unpack2<kF16>(w.y, q[2], q[3]);
+          unpack2<kF16>(w.z, q[4], q[5]);
+          unpack2<kF16>(w.w, q[6], q[7]);
+          if (!finite)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) q[y] = 1.f;
+          sts128(sb + L::kQ + (x >> 3) * (kRows * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4),
+                 pack_f16x2(q[0] * up, q[4] * up), pack_f16x2(q[1] * up, q[5] * up),
+                 pack_f16x2(q[2] * up, q[6] * up), pack_f16x2(q[3] * up, q[7] * up));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bars.q_full());
+      }
+      const int lim = p.causal && live ? len - n + tok + 1 : len;
+      const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+      const uint32_t tO = lanes + 256;
+      float m_used = -INFINITY, l = 0.f;
+      uint32_t nan_groups = 0;
+      bool ok = true;
+      for (int k = 0; k < count; ++k) {
+        const uint32_t i = tile0 + k;
+        const uint32_t tS = lanes + (i & 1) * kKeys, tP = lanes + 384 + (i & 1) * 64;
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.s_full(i & 1), (i >> 1) & 1, st,
+                                                   code(kRoleSoftmax, 1)));
+        if (!ok) break;
+        tc_fence_after();
+        if (!warp_live) {  // no row of this warp is a token: nothing of it is read
+          mbar_arrive(bars.s_free(i & 1));
+          mbar_arrive(bars.p_full(i & 1));
+          continue;
+        }
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
+        const float ct = c_row * scales[(i & 3) * 4], fv = scales[(i & 3) * 4 + 1],
+                    ev = scales[(i & 3) * 4 + 2];
+        const uint32_t found = (uint32_t)found_cells[i & 3];
+        const int key0 = (piece.t0 + k) * kKeys;
+        const bool nan_here = nan_flag[i & 3];
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bars.s_free(i & 1));
+        float s[kKeys];
+#pragma unroll
+        for (int x = 0; x < kKeys; ++x) s[x] = __uint_as_float(sr[x >> 5][x & 31]);
+        if (key0 + kKeys > all || found != 0xffu) {
+          const int left = min(lim, vis) - key0;
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x)
+            if ((x & ~15) + cell_token(x & 15) >= left || !((found >> (x >> 4)) & 1)) s[x] = -INFINITY;
+        }
+        if (nan_here)
+          for (int x = 0; x < kKeys; ++x)
+            if (key0 + (x & ~15) + cell_token(x & 15) < min(lim, vis))
+              nan_groups |= smem[L::kNan + (i & 3) * kKeys + x];
+        float mp[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mp[y] = fmaxf(s[2 * y], s[2 * y + 1]);
+#pragma unroll
+        for (int x = 8; x < kKeys; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mp[y] = fmax3(mp[y], s[x + 2 * y], s[x + 2 * y + 1]);
+        const float m_tile = fmaf(fmax3(mp[0], mp[1], fmaxf(mp[2], mp[3])), ct, ev);
+        const bool need = m_tile > m_used + kRescaleThreshold;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2_approx(m_used - m_tile);  // 0 on the first tile (m_used = -inf)
+          m_used = m_tile;
+        }
+        // P = 2^(score - m + eV)
+        const float sub = ev - (m_used == -INFINITY ? 0.f : m_used);
+        const uint64_t ct2 = f2pack(ct, ct), sub2 = f2pack(sub, sub);
+        uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+        // P V of two tiles ago has read these columns of P
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(i & 1), ((i >> 1) & 1) ^ 1, st,
+                                                   code(kRoleSoftmax, 2)));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            float a, b;
+            f2unpack(ffma2(f2pack(s[64 * half + 2 * x], s[64 * half + 2 * x + 1]), ct2, sub2), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            sum[x & 1] = fadd2(sum[x & 1], f2pack(a, b));
+            pk[x] = pack_f16x2(a, b);
+          }
+          tmem_st32(tP + 32 * half, pk);
+        }
+        float la, lb;
+        f2unpack(fadd2(sum[0], sum[1]), la, lb);
+        l = l * alpha + (la + lb) * fv;  // fv = 2^-eV
+        if (k > 0 && __any_sync(0xffffffffu, need)) {
+          // O *= alpha, once P V of the previous tile is in it
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_inl(bars.pv_done((i - 1) & 1), ((i - 1) >> 1) & 1, st,
+                                        code(kRoleSoftmax, 3)));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(tO + q * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+            tmem_st16(tO + q * 16, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bars.p_full(i & 1));
+      }
+      tmem_wait_st();
+      // ---- O / l and the log-sum-exp -------------------------------------------
+      if (ok && count > 0) {
+        const uint32_t i = tile0 + count - 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(i & 1), (i >> 1) & 1, st,
+                                                   code(kRoleSoftmax, 4)));
+        tc_fence_after();
+      }
+      if (ok) {
+        const bool whole = piece.t0 == 0 && piece.t1 == piece.tiles;
+        const bool none = count == 0 || !live || l == 0.f;  // sees no key, or is no token
+        const float inv = 1.f / l;
+        const float lse2 = none ? -INFINITY : m_used + lg2_approx(l);
+        const size_t prow = ((size_t)blockIdx.x * 2 + (pieces ? 1 : 0)) * kRows + r;
+        const bool store = !whole || tok < p.nq;
+        const size_t at = store && whole ? p.so.row(piece.b, hq, tok) : 0;
+        float *const to32 = whole ? static_cast<float *>(p.o) + at : p.part + prow * D;
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+          uint32_t o[32];
+          if (count > 0) {
+            tmem_ld32(tO + q * 32, o);
+            tmem_wait_ld();
+          }
+          const bool spoiled = (nan_groups >> q) & 1;
+          float v[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            v[x] = none      ? 0.f
+                   : spoiled ? __uint_as_float(0x7fffffffu)
+                             : __uint_as_float(o[x]) * inv;
+          if (!store) {
+          } else if (!whole || p.o_f32) {
+            float4 *const dst = reinterpret_cast<float4 *>(to32 + q * 32);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+          } else {
+            uint4 *const dst =
+                reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + at + q * 32);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[x] = make_uint4(
+                  pack2<kF16>(v[8 * x], v[8 * x + 1]), pack2<kF16>(v[8 * x + 2], v[8 * x + 3]),
+                  pack2<kF16>(v[8 * x + 4], v[8 * x + 5]), pack2<kF16>(v[8 * x + 6], v[8 * x + 7]));
+          }
+        }
+        if (store) {
+          if (whole)
+            p.lse[((size_t)piece.b * p.hq + hq) * p.nq + tok] = lse2 * kLn2;
+          else
+            p.part_lse[prow] = lse2;
+        }
+      }
+    }
+
+    // ---- the next piece ----------------------------------------------------------
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    failed = *reinterpret_cast<volatile int *>(misc) != 0;
+    if (failed) break;
+    piece.link(chain, pieces == 0);
+    tile0 += count;
+    ++pieces;
+    f = piece.next(p);
+    if (!piece.advance(p, blocks, misc, f)) break;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0 && !p.whole) p.chain[blockIdx.x] = failed ? make_int4(-1, 0, 0, 1) : chain;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kF16>
+cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
+  static std::atomic<bool> configured[64];  // per device
+  const cudaError_t e =
+      allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16>, TcLayout<D>::kAlloc, configured);
+  if (e != cudaSuccess) return e;
+  LaunchProbe probe(kKindCacheFwdTc, stream);
+  fa_cache_fwd_tc_kernel<D, kF16><<<p.ctas, kThreads, TcLayout<D>::kAlloc, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream) {
+  const bool f16 = p.pool.f16 != 0;
+  switch (p.pool.d) {
+    case 64: return f16 ? launch_tc<64, true>(p, stream) : launch_tc<64, false>(p, stream);
+    case 96: return f16 ? launch_tc<96, true>(p, stream) : launch_tc<96, false>(p, stream);
+    case 128: return f16 ? launch_tc<128, true>(p, stream) : launch_tc<128, false>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fa

@@ -133,7 +133,7 @@ enum KernelKind : int { kKindFwd = 0, kKindBwdPre = 1, kKindBwdDkdv = 2, kKindBw
                         kKindFwdCombine = 4, kKindBwd256Dv = 5, kKindBwd256Dk = 6,
                         kKindBwd256Dq = 7, kKindBwdFused = 8, kKindBwdConvert = 9,
                         kKindCacheWrite = 10, kKindCacheRead = 11, kKindCacheFwd = 12,
-                        kKindCacheCombine = 13, kNumKinds = 14 };
+                        kKindCacheCombine = 13, kKindCacheFwdTc = 14, kNumKinds = 15 };
 
 // Brackets one launch with CUDA events when measurement is enabled
 // (fa_profile_enable); a no-op otherwise.
@@ -179,7 +179,7 @@ cudaError_t launch_backward_d256(const BwdParams &p, cudaStream_t stream);
 enum KernelId : uint32_t { kKernFwd = 1, kKernBwdPre = 2, kKernBwd = 3, kKernBwdDq = 4,
                            kKernBwd256Dv = 5, kKernBwd256Dk = 6, kKernBwd256Dq = 7,
                            kKernBwdFused = 8, kKernCacheWrite = 9, kKernCacheRead = 10,
-                           kKernCacheFwd = 11 };
+                           kKernCacheFwd = 11, kKernCacheFwdTc = 12 };
 __host__ __device__ constexpr uint32_t status_code(uint32_t kernel, uint32_t role, uint32_t site) {
   return 0x80000000u | (kernel << 16) | (role << 8) | site;
 }

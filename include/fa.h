@@ -417,8 +417,8 @@ fa_status fa_debug_configure(unsigned int flags, unsigned long long wait_limit_n
  * 0 forward, 1 backward preprocess (D_i and LSE*log2 e), 2 backward dK/dV,
  * 3 backward dQ, 4 merge of a split forward, for head dimension 256 the
  * backward's 5 dV, 6 dK and 7 dQ kernels, 8 the one-pass backward and 9 its
- * dQ conversion, 10 cache write, 11 cache read, 12 attention over a cache and
- * 13 the merge of its parts; fa_kernel_name() names them ("" for an unknown id).
+ * dQ conversion, 10 cache write, 11 cache read, 12 attention over a cache (14
+ * for many query rows) and 13 the merge of its parts; fa_kernel_name() names them ("" for an unknown id).
  *
  * fa_profile_enable(1): from then on every kernel launch is bracketed by two
  * CUDA events recorded on its stream (no synchronisation, no device memory).
