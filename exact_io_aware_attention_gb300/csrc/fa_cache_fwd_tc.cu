@@ -21,12 +21,13 @@
 //            and four words a 16-byte piece of a channel's row;
 //   the columns of S and P are slots (cell_token gives their tokens).
 //
-// CTA: 12 warps, one CTA an SM, pieces of the axis of work as in
+// CTA: 16 warps, one CTA an SM, pieces of the axis of work as in
 // fa_cache_fwd.cu (the same units, scratch and merge):
 //   warp 0       bulk copies of cells into a ring of two tiles
 //   warp 1       tcgen05 issuer (one lane) and tensor-memory owner
 //   warps 4-7    Q to shared memory, softmax, output (thread = row = TMEM lane)
-//   warps 8-11   expansion of K and V
+//   warps 8-11   expansion of K
+//   warps 12-15  expansion of V
 // Tensor memory: S_0 [0,128), S_1 [128,256), O [256,256+d), P_0 [384,448),
 // P_1 [448,512). S of the next tile is issued ahead of P V of this one.
 //
@@ -42,7 +43,11 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+// registers a thread: at the launch (65536 / 512), and after the warpgroups
+// have moved them: the softmax holds a row of 128 scores
+constexpr int kRegsLaunch = 128, kRegsIssue = 96, kRegsSoftmax = 208, kRegsExpand = 104;
+static_assert(kRegsIssue + kRegsSoftmax + 2 * kRegsExpand == 4 * kRegsLaunch, "register split");
 constexpr int kRows = 128, kKeys = 128, kTileCells = kKeys / kCellTokens;
 constexpr float kRescaleThreshold = 8.0f;  // log2: m moves when P would pass 2^8
 
@@ -63,9 +68,9 @@ struct TcLayout {
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
   static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][slot] groups of V that are NaN
   static constexpr int kScales = kNan + 4 * kKeys;        // [4]: 2^eK, 2^eV, 2^-eV, eV
-  static constexpr int kFlags = kScales + 4 * 16;         // [4]: any NaN; [4] found cells; [8] reduction
+  static constexpr int kFlags = kScales + 4 * 16;         // [4] any NaN, [4] found cells, reductions
   static constexpr int kBars = kFlags + 32 + 48;
-  static constexpr int kNumBars = 18;
+  static constexpr int kNumBars = 20;
   static constexpr int kTmem = kBars + kNumBars * 8;
   static constexpr int kMisc = (kTmem + 8 + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + kWorkBytes;
@@ -86,6 +91,7 @@ struct TcBars {
   __device__ uint32_t pv_done(int s) const { return base + 8 * (14 + s); }  // and V and P are free
   __device__ uint32_t q_full() const { return base + 8 * 16; }
   __device__ uint32_t teardown() const { return base + 8 * 17; }
+  __device__ uint32_t v_scale(int s) const { return base + 8 * (18 + s); }  // eV is known
 };
 
 enum TcRole : uint32_t { kRoleLoad = 1, kRoleMma = 2, kRoleSoftmax = 3, kRoleExpand = 4 };
@@ -127,21 +133,31 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t lo2
   return hfma2(u, s2, lo2);
 }
 
-// The barrier of the expansion warps.
-__device__ __forceinline__ void expand_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The same, and whether all of them are well: they give up together, since a
-// warp that left alone would leave the others at the barrier.
-__device__ __forceinline__ bool expand_all(bool ok) {
+// The barrier of a warpgroup that expands, and whether all of its threads are
+// well: they give up together, since a warp that left alone would leave the
+// others at the barrier.
+template <int kId>
+__device__ __forceinline__ bool expand_sync(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"((uint32_t)ok)
+      : "r"((uint32_t)ok), "n"(kId)
       : "memory");
   return all != 0;
+}
+
+// The largest x of a warpgroup that expands, through `red` ([4] floats).
+template <int kId>
+__device__ __forceinline__ float expand_max(float x, volatile float *red, int dw) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  if ((threadIdx.x & 31) == 0) red[dw] = x;
+  expand_sync<kId>(true);
+  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
 
 // The power of two at or below x > 0 times 2^-7, between 2^-120 and 2^120 (1 for 0): what
@@ -173,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bars.packed_full(s), 1);
-      mbar_init(bars.packed_empty(s), 128);
+      mbar_init(bars.packed_empty(s), 256);
+      mbar_init(bars.v_scale(s), 128);
       mbar_init(bars.k_full(s), 128);
       mbar_init(bars.v_full(s), 128);
       mbar_init(bars.s_full(s), 1);
@@ -197,18 +214,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmem);
   const int heads = p.pool.heads;
-  int4 chain = make_int4(-1, 0, 0, 0);
-  long long f = mine.f;
-  uint32_t tile0 = 0, pieces = 0;  // tiles and pieces before this one: buffers and parities
-  bool failed = false;
-  while (mine.found && f < mine.f_end) {
-    const Piece piece(p, blocks, misc, f, mine.f_end);
-    if (piece.h < 0 || piece.h >= heads) break;
-    const int n = piece.n, len = piece.len, vis = piece.vis, cells = piece.cells;
-    const int count = max(0, min(piece.t1, (cells + kTileCells - 1) / kTileCells) - piece.t0);
-    // keys before `all` are visible to every row that is a token
-    const int all = p.causal ? min(vis, len - n + p.by_group.div(piece.row0) + 1) : vis;
 
+  // Every role walks over the same pieces, tiles [piece.t0, piece.t0 + count) of
+  // a segment; tile0 counts the tiles before a piece (buffers and parities).
+  // work(piece, count, tile0, pieces) ends with the barrier of all threads.
+  int4 chain = make_int4(-1, 0, 0, 0);
+  bool failed = false;
+  auto walk = [&](auto work) {
+    long long f = mine.f;
+    uint32_t tile0 = 0, pieces = 0;
+    while (mine.found && f < mine.f_end) {
+      const Piece piece(p, blocks, misc, f, mine.f_end);
+      if (piece.h < 0 || piece.h >= heads) break;
+      const int count =
+          max(0, min(piece.t1, (piece.cells + kTileCells - 1) / kTileCells) - piece.t0);
+      work(piece, count, tile0, pieces);
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      failed = *reinterpret_cast<volatile int *>(misc) != 0;
+      if (failed) break;
+      piece.link(chain, pieces == 0);
+      tile0 += count;
+      ++pieces;
+      f = piece.next(p);
+      if (!piece.advance(p, blocks, misc, f)) break;
+      __syncthreads();
+    }
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsIssue>();
+    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t pieces) {
+      const int cells = piece.cells;
     if (warp == 0) {
       // ---- copies ----------------------------------------------------------
       const int32_t *const table = p.pool.table + (size_t)((long long)piece.b * p.pool.table_stride);
@@ -301,90 +339,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp >= 8) {
-      // ---- expansion -------------------------------------------------------
-      const int dt = threadIdx.x - 256, dw = warp - 8;
-      bool ok = true;
-      for (int k = 0; k < count; ++k) {
-        const uint32_t i = tile0 + k;
-        const int slot2 = i & 1;
-        const uint32_t parity = (i >> 1) & 1;
-        const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
-        if (!expand_all(ok && mbar_wait_inl(bars.packed_full(slot2), parity, st,
-                                            code(kRoleExpand, 1))))
-          break;
-        const uint32_t found = (uint32_t)found_cells[i & 3];
-        const int key0 = (piece.t0 + k) * kKeys;
-        // s and lo of the token of K slot dt, and of one token of V: this
-        // thread's half z of pair (cell, y, t)
-        float ks[kG], kl[kG], vs[kG], vl[kG];
-        const int cell = dt >> 4, vy = (dt >> 3) & 1, vt = (dt >> 1) & 3, vz = dt & 1;
-        const uint32_t at = ring + cell * cell_bytes(D);
-        const bool there = (found >> cell) & 1;
-        const bool k_live = there && key0 + cell * kCellTokens + cell_token(dt & 15) < vis;
-        const bool v_live = there && key0 + cell * kCellTokens + vt + 8 * vy + 4 * vz < vis;
-        float k_top = 0.f, v_top = 0.f;
-        uint32_t nans = 0;
+    }
+    });
+  } else if (warp >= 8) {
+    setmaxnreg_dec<kRegsExpand>();
+    const int dt = threadIdx.x & 127, dw = warp & 3;
+    if (warp < 12) {
+      // ---- expansion of K ---------------------------------------------------
+      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t) {
+        bool ok = true;
+        for (int k = 0; k < count; ++k) {
+          const uint32_t i = tile0 + k;
+          const int slot2 = i & 1;
+          const uint32_t parity = (i >> 1) & 1;
+          const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
+          ok = expand_sync<1>(
+              ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 1)));
+          if (!ok) break;
+          const uint32_t found = (uint32_t)found_cells[i & 3];
+          {
+            // s and lo of slot dt
+            const int cell = dt >> 4;
+            const uint32_t at = ring + cell * cell_bytes(D) + k_lo<D>(dt & 15, 0);
+            float s[kG], lo[kG];
+            uint32_t w[kG];  // kG lo, then kG s, in pairs
+            if constexpr (kG == 3) {
+              lds_words<3>(at, w);
+              unpack2<kF16>(w[0], lo[0], lo[1]);
+              unpack2<kF16>(w[1], lo[2], s[0]);
+              unpack2<kF16>(w[2], s[1], s[2]);
+            } else {
+              lds_words<kG>(at, w);
 #pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          float unused;
-          (void)unused;
-          uint16_t h;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + k_s<D>(dt & 15, g)) : "memory");
-          unpack2<kF16>(h, ks[g], unused);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + k_lo<D>(dt & 15, g)) : "memory");
-          unpack2<kF16>(h, kl[g], unused);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + v_s<D>(vy, vt, g) + 2 * vz) : "memory");
-          unpack2<kF16>(h, vs[g], unused);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at + v_lo<D>(vy, vt, g) + 2 * vz) : "memory");
-          unpack2<kF16>(h, vl[g], unused);
-          if (!k_live) ks[g] = kl[g] = 0.f;
-          if (!v_live) vs[g] = vl[g] = 0.f;
-          if (!(vl[g] == vl[g])) {
-            nans |= 1u << g;
-            vs[g] = vl[g] = 0.f;
+              for (int x = 0; x < kG / 2; ++x) {
+                unpack2<kF16>(w[x], lo[2 * x], lo[2 * x + 1]);
+                unpack2<kF16>(w[kG / 2 + x], s[2 * x], s[2 * x + 1]);
+              }
+            }
+            const bool live = ((found >> cell) & 1) &&
+                              (piece.t0 + k) * kKeys + cell * kCellTokens + cell_token(dt & 15) <
+                                  piece.vis;
+            float top = 0.f;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              if (!live) s[g] = lo[g] = 0.f;
+              // (a NaN does not enter the maximum)
+              top = fmaxf(top, fmaxf(fabsf(lo[g]), fabsf(fmaf(15.f, s[g], lo[g]))));
+            }
+            const int e = tile_exponent(expand_max<1>(top, red, dw));
+            const float down = pow2(-e);
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+              sts64(sb + L::kMetaK + (dt * kG + g) * 8, pack_f16x2(s[g] * down, s[g] * down),
+                    pack_f16x2(lo[g] * down, lo[g] * down));
+            if (dt == 0) scales[(i & 3) * 4] = pow2(e);
           }
-          // (a NaN does not enter the maximum)
-          k_top = fmaxf(k_top, fmaxf(fabsf(kl[g]), fabsf(fmaf(15.f, ks[g], kl[g]))));
-          v_top = fmaxf(v_top, fmaxf(fabsf(vl[g]), fabsf(fmaf(15.f, vs[g], vl[g]))));
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          k_top = fmaxf(k_top, __shfl_xor_sync(0xffffffffu, k_top, o));
-          v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
-        }
-        const bool any_nan = __any_sync(0xffffffffu, nans != 0);
-        if (lane == 0) {
-          red[dw] = k_top;
-          red[4 + dw] = v_top;
-          red[8 + dw] = any_nan ? 1.f : 0.f;
-        }
-        expand_sync();  // (and the last tile's groups have been used)
-        const int ek = tile_exponent(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const int ev = tile_exponent(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
-        const float fk = pow2(-ek), fv = pow2(-ev);
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          const float s = ks[g] * fk, lo = kl[g] * fk;
-          sts64(sb + L::kMetaK + (dt * kG + g) * 8, pack_f16x2(s, s), pack_f16x2(lo, lo));
-          const uint32_t o = ((((cell * 2 + vy) * kG + g) * 4 + vt) * 2 + vz) * 2;
-          sts16(sb + L::kMetaV + o, pack_f16x2(vs[g] * fv, 0.f));
-          sts16(sb + L::kVLo + o, pack_f16x2(vl[g] * fv, 0.f));
-        }
-        smem[L::kNan + (i & 3) * kKeys + cell * 16 + cell_slot(vt + 8 * vy + 4 * vz)] = (uint8_t)nans;
-        if (dt == 0) {
-          nan_flag[i & 3] = red[8] + red[9] + red[10] + red[11] > 0.f;
-          scales[(i & 3) * 4] = pow2(ek);
-          scales[(i & 3) * 4 + 1] = pow2(-ev);
-          scales[(i & 3) * 4 + 2] = (float)ev;
-        }
-        expand_sync();
-
-        // K, into the buffer that S of two tiles ago has read
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_inl(bars.s_full(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
-        if (ok) {
+          // the buffer that S of two tiles ago has read
+          ok = expand_sync<1>(
+              mbar_wait_inl(bars.s_full(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
+          if (!ok) break;
           const uint32_t dst = sb + L::kK + slot2 * L::kQkBytes;
+          // eight lanes that store together: the four t, two slots four apart
           const int t = lane & 3, low = (((lane >> 2) & 1) << 2) | (lane >> 3);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -401,17 +416,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                      expand<3>(w[g], s2, lo2));
             }
           }
+          fence_proxy_async_smem();
+          mbar_arrive(bars.k_full(slot2));
+          mbar_arrive(bars.packed_empty(slot2));
         }
-        fence_proxy_async_smem();
-        if (ok) mbar_arrive(bars.k_full(slot2));
-
-        // V, into the buffer that P V of two tiles ago has read
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(slot2), parity ^ 1, st,
-                                                         code(kRoleExpand, 3)));
-        if (ok) {
+      });
+    } else {
+      // ---- expansion of V ---------------------------------------------------
+      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t) {
+        bool ok = true;
+        for (int k = 0; k < count; ++k) {
+          const uint32_t i = tile0 + k;
+          const int slot2 = i & 1;
+          const uint32_t parity = (i >> 1) & 1;
+          const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
+          // the cells, and the buffer that P V of two tiles ago has read
+          ok = expand_sync<2>(
+              ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 3)) &&
+              mbar_wait_inl(bars.pv_done(slot2), parity ^ 1, st, code(kRoleExpand, 4)));
+          if (!ok) break;
+          const uint32_t found = (uint32_t)found_cells[i & 3];
+          {
+            // s and lo of one token: half z of pair (cell, y, t)
+            const int cell = dt >> 4, y = (dt >> 3) & 1, t = (dt >> 1) & 3, z = dt & 1;
+            const uint32_t at = ring + cell * cell_bytes(D);
+            const int token = t + 8 * y + 4 * z;
+            const bool live = ((found >> cell) & 1) &&
+                              (piece.t0 + k) * kKeys + cell * kCellTokens + token < piece.vis;
+            uint32_t ws[kG], wl[kG];
+            lds_words<kG>(at + v_s<D>(y, t, 0), ws);
+            lds_words<kG>(at + v_lo<D>(y, t, 0), wl);
+            float s[kG], lo[kG], top = 0.f;
+            uint32_t nans = 0;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              unpack2<kF16>(__byte_perm(ws[g], wl[g], z ? 0x7632 : 0x5410), s[g], lo[g]);
+              if (!live) s[g] = lo[g] = 0.f;
+              if (!(lo[g] == lo[g])) {
+                nans |= 1u << g;
+                s[g] = lo[g] = 0.f;
+              }
+              top = fmaxf(top, fmaxf(fabsf(lo[g]), fabsf(fmaf(15.f, s[g], lo[g]))));
+            }
+            const bool any_nan = __any_sync(0xffffffffu, nans != 0);
+            if (lane == 0) red[8 + dw] = any_nan ? 1.f : 0.f;
+            const int e = tile_exponent(expand_max<2>(top, red + 4, dw));
+            const float down = pow2(-e);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              const uint32_t o = ((((cell * 2 + y) * kG + g) * 4 + t) * 2 + z) * 2;
+              sts16(sb + L::kMetaV + o, pack_f16x2(s[g] * down, 0.f));
+              sts16(sb + L::kVLo + o, pack_f16x2(lo[g] * down, 0.f));
+            }
+            smem[L::kNan + (i & 3) * kKeys + cell * 16 + cell_slot(token)] = (uint8_t)nans;
+            if (dt == 0) {
+              nan_flag[i & 3] = red[8] + red[9] + red[10] + red[11] > 0.f;
+              scales[(i & 3) * 4 + 1] = down;
+              scales[(i & 3) * 4 + 2] = (float)e;
+            }
+          }
+          mbar_arrive(bars.v_scale(slot2));
+          expand_sync<2>(true);
           const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
           // eight lanes that store together: four blocks of 8 slots, two r
-          const int kb = (lane & 3) | (((dw >> 0) & 3) << 2);  // block of 8 slots: cell * 2 + y
+          const int kb = (lane & 3) | (dw << 2);  // block of 8 slots: cell * 2 + y
           const int r = lane >> 2;
           const uint32_t from = ring + (kb >> 1) * cell_bytes(D);
           uint32_t w[4][kG];
@@ -434,14 +502,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             row(std::integral_constant<int, 2>{});
             row(std::integral_constant<int, 3>{});
           }
-        }
-        fence_proxy_async_smem();
-        if (ok) {
+          fence_proxy_async_smem();
           mbar_arrive(bars.v_full(slot2));
           mbar_arrive(bars.packed_empty(slot2));
         }
-      }
-    } else if (warp >= 4) {
+      });
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t pieces) {
+      const int n = piece.n, len = piece.len, vis = piece.vis;
+      // keys before `all` are visible to every row that is a token
+      const int all = p.causal ? min(vis, len - n + p.by_group.div(piece.row0) + 1) : vis;
       // ---- Q, softmax, output ------------------------------------------------
       const int r = threadIdx.x - 128;
       const int row = piece.row0 + r;
@@ -515,11 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sr[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
-        const float ct = c_row * scales[(i & 3) * 4], fv = scales[(i & 3) * 4 + 1],
-                    ev = scales[(i & 3) * 4 + 2];
+        const float ct = c_row * scales[(i & 3) * 4];
         const uint32_t found = (uint32_t)found_cells[i & 3];
         const int key0 = (piece.t0 + k) * kKeys;
-        const bool nan_here = nan_flag[i & 3];
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(bars.s_free(i & 1));
@@ -532,7 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < kKeys; ++x)
             if ((x & ~15) + cell_token(x & 15) >= left || !((found >> (x >> 4)) & 1)) s[x] = -INFINITY;
         }
-        if (nan_here)
+        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.v_scale(i & 1), (i >> 1) & 1, st,
+                                                   code(kRoleSoftmax, 5)));
+        if (!ok) break;
+        const float fv = scales[(i & 3) * 4 + 1], ev = scales[(i & 3) * 4 + 2];
+        if (nan_flag[i & 3])
           for (int x = 0; x < kKeys; ++x)
             if (key0 + (x & ~15) + cell_token(x & 15) < min(lim, vis))
               nan_groups |= smem[L::kNan + (i & 3) * kKeys + x];
@@ -611,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = 1.f / l;
         const float lse2 = none ? -INFINITY : m_used + lg2_approx(l);
         const size_t prow = ((size_t)blockIdx.x * 2 + (pieces ? 1 : 0)) * kRows + r;
-        const bool store = !whole || tok < p.nq;
+        const bool store = tok < p.nq;  // (nothing reads the other rows)
         const size_t at = store && whole ? p.so.row(piece.b, hq, tok) : 0;
         float *const to32 = whole ? static_cast<float *>(p.o) + at : p.part + prow * D;
 #pragma unroll
@@ -651,20 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.part_lse[prow] = lse2;
         }
       }
-    }
-
-    // ---- the next piece ----------------------------------------------------------
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    failed = *reinterpret_cast<volatile int *>(misc) != 0;
-    if (failed) break;
-    piece.link(chain, pieces == 0);
-    tile0 += count;
-    ++pieces;
-    f = piece.next(p);
-    if (!piece.advance(p, blocks, misc, f)) break;
-    __syncthreads();
+    });
   }
   if (threadIdx.x == 0 && !p.whole) p.chain[blockIdx.x] = failed ? make_int4(-1, 0, 0, 1) : chain;
   tc_fence_before();
@@ -681,6 +742,8 @@ cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
   const cudaError_t e =
       allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16>, TcLayout<D>::kAlloc, configured);
   if (e != cudaSuccess) return e;
+  static const cudaError_t regs = check_kernel_regs(fa_cache_fwd_tc_kernel<D, kF16>, kRegsLaunch);
+  if (regs != cudaSuccess) return regs;
   LaunchProbe probe(kKindCacheFwdTc, stream);
   fa_cache_fwd_tc_kernel<D, kF16><<<p.ctas, kThreads, TcLayout<D>::kAlloc, stream>>>(p);
   return cudaGetLastError();
