@@ -170,20 +170,23 @@ cudaError_t launch_cache_write(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream);
 
-// The attention with 128 query rows a CTA on tcgen05 (fa_cache_fwd_tc.cu), d up
-// to 128; the merge of its parts is launched by launch_cache_forward.
-cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream);
+// The attention with 128 or 256 query rows a CTA on tcgen05 (fa_cache_fwd_tc.cu),
+// d up to 128; the merge of its parts is launched by launch_cache_forward.
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows, cudaStream_t stream);
 
 // Query rows (new tokens times query heads of one K/V head) that one CTA
 // holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
-// tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 in
-// the one for many.
+// tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
+// in the one for many. Measured, 16 sequences of 6600 keys, 2 K/V heads, d = 128
+// (few / many): 24 rows 36 / 58 us, 64 rows 57 / 63 us, 96 rows 68 / 69 us (bf16)
+// and 78 / 69 us (f16), 128 rows 98 / 74 us; 4 sequences of 4000 keys, 12 heads,
+// d = 64: 64 rows 40 / 49 us, 100 rows 57 / 53 us.
 constexpr int cache_forward_block_rows(int d, long long rows) {
-  return d == 256 || rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
+  return d == 256 || rows <= 8 ? 8 : rows <= 64 ? 16 : rows <= 128 ? 128 : 256;
 }
 // CTAs that one SM holds (its registers and shared memory allow).
 constexpr int cache_forward_ctas_per_sm(int d, int block_rows) {
-  return block_rows == 128 ? 1
+  return block_rows >= 128 ? 1
          : block_rows == 8 ? (d == 256 ? 2 : d == 128 ? 3 : 4)
                            : (d == 64 ? 3 : 2);
 }

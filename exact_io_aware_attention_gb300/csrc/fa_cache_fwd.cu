@@ -790,12 +790,12 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
   if (threadIdx.x == 0 && !p.whole) p.chain[blockIdx.x] = chain;
 }
 
-// Merge of the parts of the segments that more than one CTA worked on: block
-// (x, y) merges row y of the segment that begins in attention CTA x, if there
+// Merge of the parts of the segments that more than one CTA worked on: blocks
+// (x, y) merge the rows of the segment that begins in attention CTA x, if there
 // is one:  LSE = log sum_s 2^LSE_s,  O = sum_s 2^(LSE_s - LSE) O_s.
 // A thread holds 4 columns; kSub threads share a column's parts, each every
 // kSub-th, so that a chain over the whole GPU is a few loads deep.
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 256, kCombineRows = 16;  // blocks of a segment at most
 
 template <int D, int kRows, bool kF16>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -805,13 +805,11 @@ __global__ void __launch_bounds__(kCombineThreads)
   __shared__ float s_top[kSub], s_sum[kSub];
   __shared__ int s_last;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int x = blockIdx.x, row = blockIdx.y;
+  const int x = blockIdx.x;
   const int4 c = p.chain[x];
   if (c.x < 0) return;
   const int row_blocks = (p.nq * p.group + kRows - 1) / kRows;
   const int b = p.by_row_blocks.div(c.x), row0 = (c.x - b * row_blocks) * kRows;
-  const int tok = p.by_group.div(row0 + row), hq = c.y * p.group + (row0 + row - tok * p.group);
-  if (tok >= p.nq) return;
   // the first later CTA in which the segment ends
   if (threadIdx.x == 0) s_last = p.ctas - 1;
   __syncthreads();
@@ -824,71 +822,78 @@ __global__ void __launch_bounds__(kCombineThreads)
   }
   const int last = s_last;
   const int sub = threadIdx.x / kChunks, chunk = threadIdx.x - sub * kChunks;
-  if (sub < kSub) {
-    float top = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
-    for (int s0 = x + sub; s0 <= last; s0 += kBatch * kSub) {
-      float lse2[kBatch];
-      float4 a[kBatch];
+  for (int row = blockIdx.y; row < kRows; row += gridDim.y) {
+    const int tok = p.by_group.div(row0 + row), hq = c.y * p.group + (row0 + row - tok * p.group);
+    if (tok >= p.nq) return;  // (nor are the rows behind it tokens)
+    if (sub < kSub) {
+      float top = -INFINITY, sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int kBatch = 4;
+      for (int s0 = x + sub; s0 <= last; s0 += kBatch * kSub) {
+        float lse2[kBatch];
+        float4 a[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int s = s0 + i * kSub;
-        const size_t prow = ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
-        lse2[i] = s <= last ? p.part_lse[prow] : -INFINITY;
-        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s <= last) a[i] = *reinterpret_cast<const float4 *>(p.part + prow * D + chunk * 4);
+        for (int i = 0; i < kBatch; ++i) {
+          const int s = s0 + i * kSub;
+          const size_t prow = ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
+          lse2[i] = s <= last ? p.part_lse[prow] : -INFINITY;
+          a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s <= last) a[i] = *reinterpret_cast<const float4 *>(p.part + prow * D + chunk * 4);
+        }
+        float high = top;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) high = fmaxf(high, lse2[i]);
+        if (top != -INFINITY) {
+          const float corr = ex2_approx(top - high);
+          sum *= corr;
+          o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
+        }
+        top = high;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          // (a part without keys counts nothing; a NaN goes on)
+          const float w = lse2[i] == -INFINITY ? 0.f : ex2_approx(lse2[i] - top);
+          sum += w;
+          o = make_float4(fmaf(w, a[i].x, o.x), fmaf(w, a[i].y, o.y), fmaf(w, a[i].z, o.z),
+                          fmaf(w, a[i].w, o.w));
+        }
       }
-      float high = top;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) high = fmaxf(high, lse2[i]);
-      const float corr = top == -INFINITY ? 0.f : ex2_approx(top - high);
-      if (top != -INFINITY) {
-        sum *= corr;
-        o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
-      }
-      top = high;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        // (a part without keys counts nothing; a NaN goes on)
-        const float w = lse2[i] == -INFINITY ? 0.f : ex2_approx(lse2[i] - top);
-        sum += w;
-        o = make_float4(fmaf(w, a[i].x, o.x), fmaf(w, a[i].y, o.y), fmaf(w, a[i].z, o.z),
-                        fmaf(w, a[i].w, o.w));
+      s_o[sub][chunk] = o;
+      if (chunk == 0) {
+        s_top[sub] = top;
+        s_sum[sub] = sum;
       }
     }
-    s_o[sub][chunk] = o;
-    if (chunk == 0) {
-      s_top[sub] = top;
-      s_sum[sub] = sum;
+    __syncthreads();
+    if (threadIdx.x < kChunks) {
+      float top = -INFINITY, sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) top = fmaxf(top, s_top[i]);
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) {
+        if (s_sum[i] == 0.f) continue;
+        // a NaN among a thread's parts leaves its top finite or at -inf and its sum NaN
+        const float w = s_top[i] == -INFINITY ? 1.f : ex2_approx(s_top[i] - top);
+        const float4 a = s_o[i][threadIdx.x];
+        sum = fmaf(w, s_sum[i], sum);
+        o = make_float4(fmaf(w, a.x, o.x), fmaf(w, a.y, o.y), fmaf(w, a.z, o.z),
+                        fmaf(w, a.w, o.w));
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t at = p.so.row(b, hq, tok) + threadIdx.x * 4;
+      if (p.o_f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
+            make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
+      if (threadIdx.x == 0)
+        p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
+            sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
     }
+    __syncthreads();
   }
-  __syncthreads();
-  if (threadIdx.x >= kChunks) return;
-  float top = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < kSub; ++i) top = fmaxf(top, s_top[i]);
-#pragma unroll
-  for (int i = 0; i < kSub; ++i) {
-    if (s_sum[i] == 0.f) continue;
-    // a NaN among a thread's parts leaves its top finite or at -inf and its sum NaN
-    const float w = s_top[i] == -INFINITY ? 1.f : ex2_approx(s_top[i] - top);
-    const float4 a = s_o[i][threadIdx.x];
-    sum = fmaf(w, s_sum[i], sum);
-    o = make_float4(fmaf(w, a.x, o.x), fmaf(w, a.y, o.y), fmaf(w, a.z, o.z), fmaf(w, a.w, o.w));
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const size_t at = p.so.row(b, hq, tok) + threadIdx.x * 4;
-  if (p.o_f32)
-    *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
-        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  else
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
-        make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
-  if (threadIdx.x == 0)
-    p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
-        sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
 }
 
 template <int D, int kRows, bool kF16>
@@ -897,7 +902,7 @@ cudaError_t launch_combine(const CacheFwdParams &p, cudaStream_t stream) {
   LaunchProbe probe(kKindCacheCombine, stream);
   const long long rows = (long long)p.nq * p.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < kRows ? rows : kRows));
+  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < kCombineRows ? rows : kCombineRows));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -934,11 +939,12 @@ cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
   if (shares < (double)p.ctas) p.ctas = (int)shares + 1;
   cudaError_t e;
   if constexpr (D <= 128) {
-    e = rows == 128  ? launch_cache_forward_tc(p, stream)
+    e = rows >= 128  ? launch_cache_forward_tc(p, rows, stream)
         : rows == 16 ? launch_d<D, 2, kF16>(p, stream)
                      : launch_d<D, 1, kF16>(p, stream);
     if (e != cudaSuccess || p.whole) return e;
-    return rows == 128  ? launch_combine<D, 128, kF16>(p, stream)
+    return rows == 256   ? launch_combine<D, 256, kF16>(p, stream)
+           : rows == 128 ? launch_combine<D, 128, kF16>(p, stream)
            : rows == 16 ? launch_combine<D, 16, kF16>(p, stream)
                         : launch_combine<D, 8, kF16>(p, stream);
   } else {

@@ -21,15 +21,21 @@
 //            and four words a 16-byte piece of a channel's row;
 //   the columns of S and P are slots (cell_token gives their tokens).
 //
-// CTA: 16 warps, one CTA an SM, pieces of the axis of work as in
+// CTA: 20 warps, one CTA an SM, pieces of the axis of work as in
 // fa_cache_fwd.cu (the same units, scratch and merge):
-//   warp 0       bulk copies of cells into a ring of two tiles
-//   warp 1       tcgen05 issuer (one lane) and tensor-memory owner
-//   warps 4-7    Q to shared memory, softmax, output (thread = row = TMEM lane)
-//   warps 8-11   expansion of K
-//   warps 12-15  expansion of V
-// Tensor memory: S_0 [0,128), S_1 [128,256), O [256,256+d), P_0 [384,448),
-// P_1 [448,512). S of the next tile is issued ahead of P V of this one.
+//   warp 0        bulk copies of cells into a ring of two tiles
+//   warp 1        tcgen05 issuer (one lane) and tensor-memory owner
+//   warps 4-7     softmax and output, t = 0 (thread = row = TMEM lane)
+//   warps 8-11    softmax and output, t = 1
+//   warps 12-15   expansion of K
+//   warps 16-19   expansion of V
+// The two softmax warpgroups take turns with the tensor cores, either (kNT = 2,
+// more than 128 rows a K/V head) on 128 rows each, which share every expanded
+// tile, or (kNT = 1) on the same 128 rows and every second tile of keys each,
+// with an m, l and O of their own that they merge at the end.
+// Tensor memory: S_t [128 t, +128), P_t over the first 64 of these columns once
+// they have been read, O_t [256 + t d, +d). The issue order P_t V, next S_t, per
+// t, makes the completion of S_t tell that O_t and P_t are free.
 //
 // NaN. A group of V with a non-finite element reads as NaN, but 0 times NaN
 // would spread it to rows that do not see its token. So it enters V^ as 0,
@@ -43,15 +49,17 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 512;
-// registers a thread: at the launch (65536 / 512), and after the warpgroups
-// have moved them: the softmax holds a row of 128 scores
-constexpr int kRegsLaunch = 128, kRegsIssue = 96, kRegsSoftmax = 208, kRegsExpand = 104;
-static_assert(kRegsIssue + kRegsSoftmax + 2 * kRegsExpand == 4 * kRegsLaunch, "register split");
+constexpr int kThreads = 640;
+// registers a thread: at the launch, and after the warpgroups have moved them
+// (the softmax holds half a row of scores and reads them twice, for the
+// maximum and for P)
+constexpr int kRegsLaunch = 96, kRegsIssue = 48, kRegsSoftmax = 128, kRegsExpand = 88;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand == 5 * kRegsLaunch, "register split");
+static_assert(kRegsLaunch * kThreads <= 65536, "registers of an SM");
 constexpr int kRows = 128, kKeys = 128, kTileCells = kKeys / kCellTokens;
 constexpr float kRescaleThreshold = 8.0f;  // log2: m moves when P would pass 2^8
 
-template <int D>
+template <int D, int kNT>
 struct TcLayout {
   static constexpr int kG = D / 32;
   static constexpr int kChunks = (D + 63) / 64;           // 64-channel chunks of a Q or K row
@@ -60,9 +68,10 @@ struct TcLayout {
   static constexpr int kVBytes = 2 * kVChunk;
   static constexpr int kPacked = kTileCells * cell_bytes(D);
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kQkBytes;                // two buffers
-  static constexpr int kV = kK + 2 * kQkBytes;            // two buffers
-  static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
+  static constexpr int kK = kQ + kNT * kQkBytes;          // two buffers; the merge of kNT = 1 after them
+  static constexpr int kVBufs = kNT == 2 ? 1 : 2;         // what there is room for
+  static constexpr int kV = kK + 2 * kQkBytes;
+  static constexpr int kRing = kV + kVBufs * kVBytes;     // two tiles of cells
   static constexpr int kMetaK = kRing + 2 * kPacked;      // [slot][g]: (s, s), (lo, lo) in f16
   static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
@@ -70,7 +79,7 @@ struct TcLayout {
   static constexpr int kScales = kNan + 4 * kKeys;        // [4]: 2^eK, 2^eV, 2^-eV, eV
   static constexpr int kFlags = kScales + 4 * 16;         // [4] any NaN, [4] found cells, reductions
   static constexpr int kBars = kFlags + 32 + 48;
-  static constexpr int kNumBars = 20;
+  static constexpr int kNumBars = 22;
   static constexpr int kTmem = kBars + kNumBars * 8;
   static constexpr int kMisc = (kTmem + 8 + 15) / 16 * 16;
   static constexpr int kBytes = kMisc + kWorkBytes;
@@ -84,14 +93,15 @@ struct TcBars {
   __device__ uint32_t packed_full(int s) const { return base + 8 * s; }
   __device__ uint32_t packed_empty(int s) const { return base + 8 * (2 + s); }
   __device__ uint32_t k_full(int s) const { return base + 8 * (4 + s); }
-  __device__ uint32_t v_full(int s) const { return base + 8 * (6 + s); }
-  __device__ uint32_t s_full(int s) const { return base + 8 * (8 + s); }   // and K is free
-  __device__ uint32_t s_free(int s) const { return base + 8 * (10 + s); }
-  __device__ uint32_t p_full(int s) const { return base + 8 * (12 + s); }
-  __device__ uint32_t pv_done(int s) const { return base + 8 * (14 + s); }  // and V and P are free
-  __device__ uint32_t q_full() const { return base + 8 * 16; }
-  __device__ uint32_t teardown() const { return base + 8 * 17; }
-  __device__ uint32_t v_scale(int s) const { return base + 8 * (18 + s); }  // eV is known
+  __device__ uint32_t k_free(int s) const { return base + 8 * (6 + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (8 + s); }
+  __device__ uint32_t v_free(int s) const { return base + 8 * (10 + s); }
+  __device__ uint32_t v_scale(int s) const { return base + 8 * (12 + s); }  // eV is known
+  __device__ uint32_t s_full(int t) const { return base + 8 * (14 + t); }
+  __device__ uint32_t p_full(int t) const { return base + 8 * (16 + t); }
+  __device__ uint32_t pv_done(int t) const { return base + 8 * (18 + t); }
+  __device__ uint32_t q_full() const { return base + 8 * 20; }
+  __device__ uint32_t teardown() const { return base + 8 * 21; }
 };
 
 enum TcRole : uint32_t { kRoleLoad = 1, kRoleMma = 2, kRoleSoftmax = 3, kRoleExpand = 4 };
@@ -133,19 +143,18 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t lo2
   return hfma2(u, s2, lo2);
 }
 
-// The barrier of a warpgroup that expands, and whether all of its threads are
-// well: they give up together, since a warp that left alone would leave the
-// others at the barrier.
-template <int kId>
+// A barrier of kCount threads, and whether all of them are well: they give up
+// together, since a warp that left alone would leave the others at it.
+template <int kId, int kCount = 128>
 __device__ __forceinline__ bool expand_sync(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"((uint32_t)ok), "n"(kId)
+      : "r"((uint32_t)ok), "n"(kId), "n"(kCount)
       : "memory");
   return all != 0;
 }
@@ -167,10 +176,10 @@ __device__ __forceinline__ int tile_exponent(float x) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-template <int D, bool kF16>
+template <int D, bool kF16, int kNT>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_fwd_tc_kernel(const __grid_constant__ CacheFwdParams p) {
-  using L = TcLayout<D>;
+  using L = TcLayout<D, kNT>;
   constexpr int kG = L::kG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *const smem = reinterpret_cast<uint8_t *>(
@@ -190,15 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bars.packed_full(s), 1);
       mbar_init(bars.packed_empty(s), 256);
-      mbar_init(bars.v_scale(s), 128);
       mbar_init(bars.k_full(s), 128);
+      mbar_init(bars.k_free(s), 1);
       mbar_init(bars.v_full(s), 128);
+      mbar_init(bars.v_free(s), 1);
+      mbar_init(bars.v_scale(s), 128);
       mbar_init(bars.s_full(s), 1);
-      mbar_init(bars.s_free(s), 128);
       mbar_init(bars.p_full(s), 128);
       mbar_init(bars.pv_done(s), 1);
     }
-    mbar_init(bars.q_full(), 128);
+    mbar_init(bars.q_full(), kNT * 128);
     mbar_init(bars.teardown(), 1);
     misc[0] = 0;
     fence_mbar_init();
@@ -208,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Blocks blocks{p, (p.nq * p.group + kRows - 1) / kRows, kRows};
+  constexpr int kBlockRows = kNT * kRows;
+  const Blocks blocks{p, (p.nq * p.group + kBlockRows - 1) / kBlockRows, kBlockRows};
   const Share mine = find_share<kThreads>(p, blocks, misc);
   __syncthreads();
   tc_fence_after();
@@ -295,43 +306,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one() && count > 0) {
         constexpr uint32_t kIdS = idesc_f32acc(kRows, kKeys, 0, 0, true);
         constexpr uint32_t kIdPV = idesc_f32acc(kRows, D, 0, 0, true);
-        auto issue_s = [&](uint32_t i) {
+        const bool two = kNT == 2 && piece.row0 + kRows < p.nq * p.group;  // t = 1 has rows
+        auto issue_s = [&](int t, uint32_t i) {
+          const uint32_t q_base = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQkBytes;
           const uint32_t k_base = sb + L::kK + (i & 1) * L::kQkBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
-            mma_f16kind_ss(tmem + (i & 1) * kKeys, sdesc_sw128(sb + L::kQ + off, 16, 1024),
+            mma_f16kind_ss(tmem + t * kKeys, sdesc_sw128(q_base + off, 16, 1024),
                            sdesc_sw128(k_base + off, 16, 1024), kIdS, kk > 0);
           }
-          mma_commit(bars.s_full(i & 1));
+          mma_commit(bars.s_full(t));
         };
-        bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1)) &&
-                  mbar_wait_inl(bars.k_full(tile0 & 1), (tile0 >> 1) & 1, st, code(kRoleMma, 2));
-        if (ok) {
-          tc_fence_after();
-          issue_s(tile0);
-        }
-        for (int k = 0; k < count && ok; ++k) {
-          const uint32_t i = tile0 + k;
-          if (k + 1 < count) {
-            const uint32_t j = i + 1;
-            ok = mbar_wait_inl(bars.k_full(j & 1), (j >> 1) & 1, st, code(kRoleMma, 3)) &&
-                 mbar_wait_inl(bars.s_free(j & 1), ((j >> 1) & 1) ^ 1, st, code(kRoleMma, 4));
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(j);
-          }
-          ok = mbar_wait_inl(bars.v_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 5)) &&
-               mbar_wait_inl(bars.p_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 6));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v_base = sb + L::kV + (i & 1) * L::kVBytes;
+        auto issue_pv = [&](int t, uint32_t i, bool first) {
+          const uint32_t v_base = sb + L::kV + (i % L::kVBufs) * L::kVBytes;
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16kind_ts(tmem + 256, tmem + 384 + (i & 1) * 64 + kk * 8,
+            mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kKeys + kk * 8,
                            sdesc_sw128(v_base + (kk >> 2) * L::kVChunk + (kk & 3) * 32, 16, 1024),
-                           kIdPV, (k > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(bars.pv_done(i & 1));
+                           kIdPV, (!first || kk > 0) ? 1u : 0u);
+          mma_commit(bars.pv_done(t));
+        };
+        // S of tile i, for both t or for the t whose turn it is
+        auto issue_scores = [&](uint32_t i) {
+          if (!mbar_wait_inl(bars.k_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 2))) return false;
+          tc_fence_after();
+          if (kNT == 1) {
+            issue_s(i & 1, i);
+            mma_commit(bars.k_free(i & 1));
+          }
+          return true;
+        };
+        bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1));
+        if constexpr (kNT == 2) {
+          ok = ok && issue_scores(tile0);
+          if (ok) {
+            issue_s(0, tile0);
+            if (two) issue_s(1, tile0);
+            mma_commit(bars.k_free(tile0 & 1));
+          }
+          for (int k = 0; k < count && ok; ++k) {
+            const uint32_t i = tile0 + k;
+            const bool more = k + 1 < count;
+            ok = mbar_wait_inl(bars.v_full(0), i & 1, st, code(kRoleMma, 3)) &&
+                 (!more || issue_scores(i + 1));
+            for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
+              ok = mbar_wait_inl(bars.p_full(t), i & 1, st, code(kRoleMma, 4 + t));
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(t, i, k == 0);
+              if (more) issue_s(t, i + 1);
+            }
+            if (!ok) break;
+            mma_commit(bars.v_free(0));
+            if (more) mma_commit(bars.k_free((i + 1) & 1));
+          }
+        } else {
+          ok = ok && issue_scores(tile0) && (count == 1 || issue_scores(tile0 + 1));
+          for (int k = 0; k < count && ok; ++k) {
+            const uint32_t i = tile0 + k;
+            const int t = i & 1;
+            ok = mbar_wait_inl(bars.v_full(t), (i >> 1) & 1, st, code(kRoleMma, 3)) &&
+                 mbar_wait_inl(bars.p_full(t), (i >> 1) & 1, st, code(kRoleMma, 4));
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, i, k < 2);
+            mma_commit(bars.v_free(t));
+            if (k + 2 < count) ok = issue_scores(i + 2);
+          }
         }
         if (!ok) {  // gave up: what was issued ends before the tensor memory goes
           mma_commit(bars.teardown());
@@ -341,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     });
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     setmaxnreg_dec<kRegsExpand>();
     const int dt = threadIdx.x & 127, dw = warp & 3;
-    if (warp < 12) {
+    if (warp < 16) {
       // ---- expansion of K ---------------------------------------------------
       walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t) {
         bool ok = true;
@@ -396,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // the buffer that S of two tiles ago has read
           ok = expand_sync<1>(
-              mbar_wait_inl(bars.s_full(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
+              mbar_wait_inl(bars.k_free(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
           if (!ok) break;
           const uint32_t dst = sb + L::kK + slot2 * L::kQkBytes;
           // eight lanes that store together: the four t, two slots four apart
@@ -430,10 +472,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot2 = i & 1;
           const uint32_t parity = (i >> 1) & 1;
           const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
-          // the cells, and the buffer that P V of two tiles ago has read
+          const int buf = i % L::kVBufs;
+          // the cells; the buffer that P V of an earlier tile has read: with two
+          // of them before this tile's scales go out (the softmax of two tiles ago
+          // has then seen its own), with one after
+          auto wait_free = [&] {
+            return mbar_wait_inl(bars.v_free(buf), ((i / L::kVBufs) & 1) ^ 1, st,
+                                 code(kRoleExpand, 4));
+          };
           ok = expand_sync<2>(
               ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 3)) &&
-              mbar_wait_inl(bars.pv_done(slot2), parity ^ 1, st, code(kRoleExpand, 4)));
+              (kNT == 2 || wait_free()));
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
           {
@@ -476,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mbar_arrive(bars.v_scale(slot2));
-          expand_sync<2>(true);
-          const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
+          ok = expand_sync<2>(kNT == 1 || wait_free());
+          if (!ok) break;
+          const uint32_t dst = sb + L::kV + buf * L::kVBytes;
           // eight lanes that store together: four blocks of 8 slots, two r
           const int kb = (lane & 3) | (dw << 2);  // block of 8 slots: cell * 2 + y
           const int r = lane >> 2;
@@ -503,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row(std::integral_constant<int, 3>{});
           }
           fence_proxy_async_smem();
-          mbar_arrive(bars.v_full(slot2));
+          mbar_arrive(bars.v_full(buf));
           mbar_arrive(bars.packed_empty(slot2));
         }
       });
@@ -515,11 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys before `all` are visible to every row that is a token
       const int all = p.causal ? min(vis, len - n + p.by_group.div(piece.row0) + 1) : vis;
       // ---- Q, softmax, output ------------------------------------------------
-      const int r = threadIdx.x - 128;
-      const int row = piece.row0 + r;
+      const int t = (warp - 4) >> 2, r = threadIdx.x & 127;
+      const int tile_row0 = piece.row0 + (kNT == 2 ? t * kRows : 0), row = tile_row0 + r;
       const int tok = p.by_group.div(row), hq = piece.h * p.group + (row - tok * p.group);
       const bool live = tok < n;
-      const bool warp_live = p.by_group.div(piece.row0 + (warp - 4) * 32) < n;  // its first row's token
+      const bool warp_live = p.by_group.div(tile_row0 + (warp & 3) * 32) < n;  // its first row's token
+      const bool has_rows = kNT == 1 || t == 0 || tile_row0 < p.nq * p.group;
       float c_row = 0.f;
       {
         // the row scaled by a power of two, its largest element below 2^11
@@ -559,48 +610,65 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!finite)
 #pragma unroll
             for (int y = 0; y < 8; ++y) q[y] = 1.f;
-          sts128(sb + L::kQ + (x >> 3) * (kRows * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4),
-                 pack_f16x2(q[0] * up, q[4] * up), pack_f16x2(q[1] * up, q[5] * up),
-                 pack_f16x2(q[2] * up, q[6] * up), pack_f16x2(q[3] * up, q[7] * up));
+          if (kNT == 2 || t == 0)
+            sts128(sb + L::kQ + (kNT == 2 ? t : 0) * L::kQkBytes + (x >> 3) * (kRows * 128) +
+                       r * 128 + (((x & 7) ^ (r & 7)) << 4),
+                   pack_f16x2(q[0] * up, q[4] * up), pack_f16x2(q[1] * up, q[5] * up),
+                   pack_f16x2(q[2] * up, q[6] * up), pack_f16x2(q[3] * up, q[7] * up));
         }
         fence_proxy_async_smem();
-        mbar_arrive(bars.q_full());
+        if (kNT == 2 || t == 0) mbar_arrive(bars.q_full());
       }
       const int lim = p.causal && live ? len - n + tok + 1 : len;
       const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
-      const uint32_t tO = lanes + 256;
+      const uint32_t tS = lanes + t * kKeys, tO = lanes + 256 + t * D;
       float m_used = -INFINITY, l = 0.f;
       uint32_t nan_groups = 0;
       bool ok = true;
-      for (int k = 0; k < count; ++k) {
+      bool any = false;
+      for (int k = kNT == 1 ? ((tile0 ^ t) & 1) : 0; k < count && has_rows; k += kNT == 1 ? 2 : 1) {
         const uint32_t i = tile0 + k;
-        const uint32_t tS = lanes + (i & 1) * kKeys, tP = lanes + 384 + (i & 1) * 64;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.s_full(i & 1), (i >> 1) & 1, st,
-                                                   code(kRoleSoftmax, 1)));
+        const uint32_t parity = (kNT == 1 ? i >> 1 : i) & 1;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_inl(bars.s_full(t), parity, st, code(kRoleSoftmax, 1)));
         if (!ok) break;
         tc_fence_after();
         if (!warp_live) {  // no row of this warp is a token: nothing of it is read
-          mbar_arrive(bars.s_free(i & 1));
-          mbar_arrive(bars.p_full(i & 1));
+          mbar_arrive(bars.p_full(t));
+          any = true;
           continue;
         }
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
         const float ct = c_row * scales[(i & 3) * 4];
         const uint32_t found = (uint32_t)found_cells[i & 3];
         const int key0 = (piece.t0 + k) * kKeys;
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(bars.s_free(i & 1));
-        float s[kKeys];
+        const bool masked = key0 + kKeys > all || found != 0xffu;
+        const int left = min(lim, vis) - key0;
+        // scores of keys 64 half .. 64 half + 63 (slots), hidden ones -inf
+        auto load_scores = [&](int half, float (&x64)[64]) {
+          uint32_t sr[2][32];
+          tmem_ld32(tS + half * 64, sr[0]);
+          tmem_ld32(tS + half * 64 + 32, sr[1]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < kKeys; ++x) s[x] = __uint_as_float(sr[x >> 5][x & 31]);
-        if (key0 + kKeys > all || found != 0xffu) {
-          const int left = min(lim, vis) - key0;
+          for (int x = 0; x < 64; ++x) x64[x] = __uint_as_float(sr[x >> 5][x & 31]);
+          if (masked) {
+            const int from = left - half * 64;
+            const uint32_t cells4 = found >> (half * 4);
 #pragma unroll
-          for (int x = 0; x < kKeys; ++x)
-            if ((x & ~15) + cell_token(x & 15) >= left || !((found >> (x >> 4)) & 1)) s[x] = -INFINITY;
+            for (int x = 0; x < 64; ++x)
+              if ((x & ~15) + cell_token(x & 15) >= from || !((cells4 >> (x >> 4)) & 1))
+                x64[x] = -INFINITY;
+          }
+        };
+        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x64[64];
+          load_scores(half, x64);
+#pragma unroll
+          for (int x = 0; x < 64; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mp[y] = fmax3(mp[y], x64[x + 2 * y], x64[x + 2 * y + 1]);
         }
         ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.v_scale(i & 1), (i >> 1) & 1, st,
                                                    code(kRoleSoftmax, 5)));
@@ -608,15 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float fv = scales[(i & 3) * 4 + 1], ev = scales[(i & 3) * 4 + 2];
         if (nan_flag[i & 3])
           for (int x = 0; x < kKeys; ++x)
-            if (key0 + (x & ~15) + cell_token(x & 15) < min(lim, vis))
+            if ((x & ~15) + cell_token(x & 15) < left)
               nan_groups |= smem[L::kNan + (i & 3) * kKeys + x];
-        float mp[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) mp[y] = fmaxf(s[2 * y], s[2 * y + 1]);
-#pragma unroll
-        for (int x = 8; x < kKeys; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mp[y] = fmax3(mp[y], s[x + 2 * y], s[x + 2 * y + 1]);
         const float m_tile = fmaf(fmax3(mp[0], mp[1], fmaxf(mp[2], mp[3])), ct, ev);
         const bool need = m_tile > m_used + kRescaleThreshold;
         float alpha = 1.f;
@@ -624,39 +685,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           alpha = ex2_approx(m_used - m_tile);  // 0 on the first tile (m_used = -inf)
           m_used = m_tile;
         }
-        // P = 2^(score - m + eV)
+        // P = 2^(score - m + eV), over columns of S that have been read twice
         const float sub = ev - (m_used == -INFINITY ? 0.f : m_used);
         const uint64_t ct2 = f2pack(ct, ct), sub2 = f2pack(sub, sub);
         uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-        // P V of two tiles ago has read these columns of P
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(i & 1), ((i >> 1) & 1) ^ 1, st,
-                                                   code(kRoleSoftmax, 2)));
-        if (!ok) break;
-        tc_fence_after();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          float x64[64];
+          load_scores(half, x64);
           uint32_t pk[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             float a, b;
-            f2unpack(ffma2(f2pack(s[64 * half + 2 * x], s[64 * half + 2 * x + 1]), ct2, sub2), a, b);
+            f2unpack(ffma2(f2pack(x64[2 * x], x64[2 * x + 1]), ct2, sub2), a, b);
             a = ex2_approx(a);
             b = ex2_approx(b);
             sum[x & 1] = fadd2(sum[x & 1], f2pack(a, b));
             pk[x] = pack_f16x2(a, b);
           }
-          tmem_st32(tP + 32 * half, pk);
+          tmem_st32(tS + 32 * half, pk);
         }
         float la, lb;
         f2unpack(fadd2(sum[0], sum[1]), la, lb);
         l = l * alpha + (la + lb) * fv;  // fv = 2^-eV
-        if (k > 0 && __any_sync(0xffffffffu, need)) {
-          // O *= alpha, once P V of the previous tile is in it
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_inl(bars.pv_done((i - 1) & 1), ((i - 1) >> 1) & 1, st,
-                                        code(kRoleSoftmax, 3)));
-          if (!ok) break;
-          tc_fence_after();
+        if (any && __any_sync(0xffffffffu, need)) {
+          // O *= alpha: P V of this t's previous tile is in it, having been issued
+          // before this tile's S
 #pragma unroll
           for (int q = 0; q < D / 16; ++q) {
             uint32_t o[16];
@@ -669,22 +723,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bars.p_full(i & 1));
+        mbar_arrive(bars.p_full(t));
+        any = true;
       }
       tmem_wait_st();
       // ---- O / l and the log-sum-exp -------------------------------------------
-      if (ok && count > 0) {
-        const uint32_t i = tile0 + count - 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(i & 1), (i >> 1) & 1, st,
-                                                   code(kRoleSoftmax, 4)));
+      if constexpr (kNT == 2) {
+        if (ok && any)
+          ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(t), (tile0 + count - 1) & 1, st,
+                                                     code(kRoleSoftmax, 2)));
         tc_fence_after();
+      } else {
+        // the last tiles of both warpgroups: O is complete, K's buffers are free
+        for (int back = 1; back <= 2 && back <= count && ok; ++back) {
+          const uint32_t i = tile0 + count - back;
+          ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(i & 1), (i >> 1) & 1, st,
+                                                     code(kRoleSoftmax, 3)));
+        }
+        tc_fence_after();
+        // t = 1 hands m, l, O and the NaN groups over, [column / 4][row]
+        float4 *const hand = reinterpret_cast<float4 *>(smem + L::kK);
+        float *const stat = reinterpret_cast<float *>(smem + L::kMetaK);  // [3][row]
+        if (t == 1 && ok) {
+          stat[r] = any && warp_live ? m_used : -INFINITY;
+          stat[kRows + r] = l;
+          stat[2 * kRows + r] = __uint_as_float(nan_groups);
+          if (any && warp_live) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + q * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                hand[(q * 4 + x) * kRows + r] =
+                    make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+            }
+          }
+        }
+        ok = expand_sync<3, 256>(ok);
+        if (t == 0 && ok && warp_live) {
+          const float m1 = stat[r], l1 = stat[kRows + r];
+          nan_groups |= __float_as_uint(stat[2 * kRows + r]);
+          const float top = fmaxf(m_used, m1);  // (-inf: no key, or only NaN scores)
+          const float w0 = top == m_used ? 1.f : ex2_approx(m_used - top);
+          const float w1 = top == m1 ? 1.f : ex2_approx(m1 - top);
+          const bool other = count > 1 || !any;  // t = 1 had a tile
+          if (other) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + q * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float4 a = hand[(q * 4 + x) * kRows + r];
+                const float b4[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const float own = any ? __uint_as_float(o[4 * x + y]) : 0.f;
+                  o[4 * x + y] = __float_as_uint(own * w0 + b4[y] * w1);
+                }
+              }
+              tmem_st16(tO + q * 16, o);
+            }
+            tmem_wait_st();
+            l = (any ? l * w0 : 0.f) + l1 * w1;
+          }
+          m_used = top;
+        }
       }
-      if (ok) {
+      if (ok && has_rows && (kNT == 2 || t == 0)) {
         const bool whole = piece.t0 == 0 && piece.t1 == piece.tiles;
         const bool none = count == 0 || !live || l == 0.f;  // sees no key, or is no token
         const float inv = 1.f / l;
         const float lse2 = none ? -INFINITY : m_used + lg2_approx(l);
-        const size_t prow = ((size_t)blockIdx.x * 2 + (pieces ? 1 : 0)) * kRows + r;
+        const size_t prow = ((size_t)blockIdx.x * 2 + (pieces ? 1 : 0)) * kBlockRows + (row - piece.row0);
         const bool store = tok < p.nq;  // (nothing reads the other rows)
         const size_t at = store && whole ? p.so.row(piece.b, hq, tok) : 0;
         float *const to32 = whole ? static_cast<float *>(p.o) + at : p.part + prow * D;
@@ -736,27 +851,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, int kNT>
 cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
   static std::atomic<bool> configured[64];  // per device
   const cudaError_t e =
-      allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16>, TcLayout<D>::kAlloc, configured);
+      allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16, kNT>, TcLayout<D, kNT>::kAlloc, configured);
   if (e != cudaSuccess) return e;
-  static const cudaError_t regs = check_kernel_regs(fa_cache_fwd_tc_kernel<D, kF16>, kRegsLaunch);
+  static const cudaError_t regs = check_kernel_regs(fa_cache_fwd_tc_kernel<D, kF16, kNT>, kRegsLaunch);
   if (regs != cudaSuccess) return regs;
   LaunchProbe probe(kKindCacheFwdTc, stream);
-  fa_cache_fwd_tc_kernel<D, kF16><<<p.ctas, kThreads, TcLayout<D>::kAlloc, stream>>>(p);
+  fa_cache_fwd_tc_kernel<D, kF16, kNT><<<p.ctas, kThreads, TcLayout<D, kNT>::kAlloc, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, bool kF16>
+cudaError_t launch_tc_rows(const CacheFwdParams &p, bool two, cudaStream_t stream) {
+  return two ? launch_tc<D, kF16, 2>(p, stream) : launch_tc<D, kF16, 1>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream) {
-  const bool f16 = p.pool.f16 != 0;
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows,
+                                    cudaStream_t stream) {
+  const bool f16 = p.pool.f16 != 0, two = block_rows == 256;
   switch (p.pool.d) {
-    case 64: return f16 ? launch_tc<64, true>(p, stream) : launch_tc<64, false>(p, stream);
-    case 96: return f16 ? launch_tc<96, true>(p, stream) : launch_tc<96, false>(p, stream);
-    case 128: return f16 ? launch_tc<128, true>(p, stream) : launch_tc<128, false>(p, stream);
+    case 64: return f16 ? launch_tc_rows<64, true>(p, two, stream) : launch_tc_rows<64, false>(p, two, stream);
+    case 96: return f16 ? launch_tc_rows<96, true>(p, two, stream) : launch_tc_rows<96, false>(p, two, stream);
+    case 128: return f16 ? launch_tc_rows<128, true>(p, two, stream) : launch_tc_rows<128, false>(p, two, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -15,7 +15,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // Words of shared memory that find_share and Piece use: [0] abort flag, [2..7]
 // the block of the next piece: number, new tokens, length, visible keys, begin
-// (64 bits), [8..23] scan.
+// (64 bits), [8..31] scan.
 constexpr int kWorkBytes = 128;
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -93,7 +93,7 @@ template <int kThreads>
 __device__ __forceinline__ Share find_share(const CacheFwdParams &p, const Blocks &blocks,
                                             int *misc) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps <= 16, "scan words");
+  static_assert(kWarps <= 24, "scan words");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_blocks = p.B * blocks.row_blocks;
   long long total = 0;

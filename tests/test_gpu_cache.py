@@ -232,12 +232,14 @@ def test_chunks_of_a_prompt(d, Nq, Hq, Hk):
 @pytest.mark.parametrize("d", [64, 96, 128])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("B,Hq,Hk,Nq,lengths,page,counts", [
-    (1, 17, 1, 1, [1], 16, None),                       # one token, 17 heads on one
-    (2, 8, 1, 3, [5, 200], 48, [3, 0]),                 # 24 rows, an empty sequence of a batch
+    (1, 65, 1, 1, [1], 16, None),                       # one token, 65 heads on one
+    (2, 24, 1, 3, [5, 200], 48, [3, 0]),                # 72 rows, an empty sequence of a batch
     (3, 20, 2, 40, [40, 300, 10], 16, [40, 7, 39]),     # 400 rows; more new tokens than tokens
-    (1, 4, 1, 33, [1400], 128, None),                   # split between CTAs
+    (1, 4, 1, 32, [1400], 128, None),                   # 128 rows; split between CTAs
     (2, 3, 1, 50, [129, 128], 64, None),                # tiles of 128 keys that end and begin
     (1, 6, 3, 150, [2000], 80, None),
+    (1, 3, 1, 43, [2600], 64, None),                    # 129 rows: the second 128 hold one
+    (5, 3, 1, 100, [1300, 128, 127, 700, 100], 32, None),  # pieces that begin at odd tiles
 ])
 def test_many_rows(d, dtype, B, Hq, Hk, Nq, lengths, page, counts):
     for causal in (True, False):
@@ -250,7 +252,7 @@ def test_many_rows(d, dtype, B, Hq, Hk, Nq, lengths, page, counts):
 def test_sizes_of_values(v_scale, k_scale):
     """V far from 1 (the weights p s must keep their bits), sharp and flat scores."""
     attend_case(2, 4, 2, 2, [333, 40], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
-    attend_case(1, 20, 1, 2, [333], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
+    attend_case(1, 40, 1, 2, [333], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
     if 1e-4 < v_scale < 1e3 and k_scale > 1e-4:
         attend_case(2, 4, 2, 2, [333, 40], 64, 32, F16, True, v_scale=v_scale, k_scale=k_scale)
 
@@ -315,7 +317,8 @@ def test_strided_queries_and_outputs():
     compare(o, lse, q.permute(0, 2, 1, 3), k, v, lengths, None, True, None, "strided")
 
 
-@pytest.mark.parametrize("d,Hq", [(64, 2), (96, 2), (128, 2), (256, 2), (64, 7), (96, 9), (128, 36)])
+@pytest.mark.parametrize("d,Hq", [(64, 2), (96, 2), (128, 2), (256, 2), (64, 17), (96, 20),
+                                  (128, 36)])
 def test_non_finite_values_stay_where_they_are_seen(d, Hq):
     """NaN and infinities in a key or value reach only the rows that see it, and only its
     group's outputs where it is a value; a NaN query spoils its own row alone."""
@@ -601,7 +604,7 @@ def test_bad_indices_are_skipped_and_reported():
     assert lib.fa_status_string(6) == b"FA_ERR_BAD_INDEX"
 
 
-@pytest.mark.parametrize("d,Nq", [(64, 1), (128, 9), (256, 1)])
+@pytest.mark.parametrize("d,Nq", [(64, 1), (128, 9), (256, 1), (64, 40), (128, 100)])
 def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
     lib = binding.load_library()
     c, table, q, k, v = attend_case(1, 2, 1, Nq, [500], d, 64, BF16, True)
