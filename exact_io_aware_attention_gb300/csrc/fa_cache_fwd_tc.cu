@@ -68,10 +68,14 @@ struct TcLayout {
   static constexpr int kVBytes = 2 * kVChunk;
   static constexpr int kPacked = kTileCells * cell_bytes(D);
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kNT * kQkBytes;          // two buffers; the merge of kNT = 1 after them
-  static constexpr int kVBufs = kNT == 2 ? 1 : 2;         // what there is room for
-  static constexpr int kV = kK + 2 * kQkBytes;
-  static constexpr int kRing = kV + kVBufs * kVBytes;     // two tiles of cells
+  // Buffers of K and V tiles: with 256 rows there is room for three. K's is free
+  // as soon as both S have been issued, V's only after both P V, a step later
+  // (measured with one of V and two of K: 2.5 us a tile, the expansion of V waiting
+  // for the products and they for it).
+  static constexpr int kKBufs = kNT == 2 ? 1 : 2;
+  static constexpr int kK = kQ + kNT * kQkBytes;          // (kNT = 1: the merge's O later)
+  static constexpr int kV = kK + kKBufs * kQkBytes;       // two buffers
+  static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
   static constexpr int kMetaK = kRing + 2 * kPacked;      // [slot][g]: (s, s), (lo, lo) in f16
   static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
@@ -307,62 +311,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = idesc_f32acc(kRows, kKeys, 0, 0, true);
         constexpr uint32_t kIdPV = idesc_f32acc(kRows, D, 0, 0, true);
         const bool two = kNT == 2 && piece.row0 + kRows < p.nq * p.group;  // t = 1 has rows
+        // (a descriptor's low bits are the address in units of 16 bytes)
+        const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);
+        const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(sb + L::kV, 16, 1024);
         auto issue_s = [&](int t, uint32_t i) {
-          const uint32_t q_base = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQkBytes;
-          const uint32_t k_base = sb + L::kK + (i & 1) * L::kQkBytes;
+          const uint64_t q = q_desc + (kNT == 2 ? t : 0) * (L::kQkBytes >> 4);
+          const uint64_t k = k_desc + (i % L::kKBufs) * (L::kQkBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
-            mma_f16kind_ss(tmem + t * kKeys, sdesc_sw128(q_base + off, 16, 1024),
-                           sdesc_sw128(k_base + off, 16, 1024), kIdS, kk > 0);
+            const int off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+            mma_f16kind_ss(tmem + t * kKeys, q + off, k + off, kIdS, kk > 0);
           }
           mma_commit(bars.s_full(t));
         };
         auto issue_pv = [&](int t, uint32_t i, bool first) {
-          const uint32_t v_base = sb + L::kV + (i % L::kVBufs) * L::kVBytes;
+          const uint64_t v = v_desc + (i & 1) * (L::kVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
             mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kKeys + kk * 8,
-                           sdesc_sw128(v_base + (kk >> 2) * L::kVChunk + (kk & 3) * 32, 16, 1024),
-                           kIdPV, (!first || kk > 0) ? 1u : 0u);
+                           v + (((kk >> 2) * L::kVChunk + (kk & 3) * 32) >> 4), kIdPV,
+                           (!first || kk > 0) ? 1u : 0u);
           mma_commit(bars.pv_done(t));
         };
-        // S of tile i, for both t or for the t whose turn it is
-        auto issue_scores = [&](uint32_t i) {
-          if (!mbar_wait_inl(bars.k_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 2))) return false;
+        auto k_here = [&](uint32_t i) {
+          const bool here = mbar_wait_inl(bars.k_full(i % L::kKBufs), (i / L::kKBufs) & 1, st,
+                                          code(kRoleMma, 2));
           tc_fence_after();
-          if (kNT == 1) {
-            issue_s(i & 1, i);
-            mma_commit(bars.k_free(i & 1));
-          }
-          return true;
+          return here;
         };
-        bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1));
+        bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1)) && k_here(tile0);
         if constexpr (kNT == 2) {
-          ok = ok && issue_scores(tile0);
           if (ok) {
             issue_s(0, tile0);
             if (two) issue_s(1, tile0);
-            mma_commit(bars.k_free(tile0 & 1));
+            mma_commit(bars.k_free(0));
           }
           for (int k = 0; k < count && ok; ++k) {
             const uint32_t i = tile0 + k;
             const bool more = k + 1 < count;
-            ok = mbar_wait_inl(bars.v_full(0), i & 1, st, code(kRoleMma, 3)) &&
-                 (!more || issue_scores(i + 1));
+            ok = mbar_wait_inl(bars.v_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 3));
             for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
               ok = mbar_wait_inl(bars.p_full(t), i & 1, st, code(kRoleMma, 4 + t));
               if (!ok) break;
               tc_fence_after();
               issue_pv(t, i, k == 0);
-              if (more) issue_s(t, i + 1);
+              if (!more) continue;
+              ok = t > 0 || k_here(i + 1);
+              if (ok) issue_s(t, i + 1);
             }
             if (!ok) break;
-            mma_commit(bars.v_free(0));
-            if (more) mma_commit(bars.k_free((i + 1) & 1));
+            mma_commit(bars.v_free(i & 1));
+            if (more) mma_commit(bars.k_free(0));
           }
         } else {
-          ok = ok && issue_scores(tile0) && (count == 1 || issue_scores(tile0 + 1));
+          // S of tile i for the t whose turn it is
+          auto issue_turn = [&](uint32_t i) {
+            issue_s(i & 1, i);
+            mma_commit(bars.k_free(i & 1));
+          };
+          if (ok) issue_turn(tile0);
+          if (ok && count > 1) {
+            ok = k_here(tile0 + 1);
+            if (ok) issue_turn(tile0 + 1);
+          }
           for (int k = 0; k < count && ok; ++k) {
             const uint32_t i = tile0 + k;
             const int t = i & 1;
@@ -372,7 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             issue_pv(t, i, k < 2);
             mma_commit(bars.v_free(t));
-            if (k + 2 < count) ok = issue_scores(i + 2);
+            if (k + 2 < count) {
+              ok = k_here(i + 2);
+              if (ok) issue_turn(i + 2);
+            }
           }
         }
         if (!ok) {  // gave up: what was issued ends before the tensor memory goes
@@ -436,14 +451,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pack_f16x2(lo[g] * down, lo[g] * down));
             if (dt == 0) scales[(i & 3) * 4] = pow2(e);
           }
-          // the buffer that S of two tiles ago has read
+          // the buffer that S of an earlier tile has read
           ok = expand_sync<1>(
-              mbar_wait_inl(bars.k_free(slot2), parity ^ 1, st, code(kRoleExpand, 2)));
+              mbar_wait_inl(bars.k_free(i % L::kKBufs), ((i / L::kKBufs) & 1) ^ 1, st,
+                            code(kRoleExpand, 2)));
           if (!ok) break;
-          const uint32_t dst = sb + L::kK + slot2 * L::kQkBytes;
+          const uint32_t dst = sb + L::kK + (i % L::kKBufs) * L::kQkBytes;
           // eight lanes that store together: the four t, two slots four apart
           const int t = lane & 3, low = (((lane >> 2) & 1) << 2) | (lane >> 3);
-#pragma unroll
+// (loops of the roles stay rolled: together they are more code than the
+          // instruction cache holds; measured 12 % on a chunk of 1024 tokens)
+#pragma unroll 1
           for (int x = 0; x < 4; ++x) {
             const int slot = (dw * 4 + x) * 8 + low;
             uint32_t w[kG];
@@ -459,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(bars.k_full(slot2));
+          mbar_arrive(bars.k_full(i % L::kKBufs));
           mbar_arrive(bars.packed_empty(slot2));
         }
       });
@@ -472,17 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot2 = i & 1;
           const uint32_t parity = (i >> 1) & 1;
           const uint32_t ring = sb + L::kRing + slot2 * L::kPacked;
-          const int buf = i % L::kVBufs;
-          // the cells; the buffer that P V of an earlier tile has read: with two
-          // of them before this tile's scales go out (the softmax of two tiles ago
-          // has then seen its own), with one after
-          auto wait_free = [&] {
-            return mbar_wait_inl(bars.v_free(buf), ((i / L::kVBufs) & 1) ^ 1, st,
-                                 code(kRoleExpand, 4));
-          };
+          // the cells, and the buffer that P V of two tiles ago has read (whose
+          // softmax has then seen its own scales: their barrier has two places)
           ok = expand_sync<2>(
               ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 3)) &&
-              (kNT == 2 || wait_free()));
+              mbar_wait_inl(bars.v_free(slot2), parity ^ 1, st, code(kRoleExpand, 4)));
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
           {
@@ -525,18 +537,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mbar_arrive(bars.v_scale(slot2));
-          ok = expand_sync<2>(kNT == 1 || wait_free());
-          if (!ok) break;
-          const uint32_t dst = sb + L::kV + buf * L::kVBytes;
+          expand_sync<2>(true);
+          const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
           // eight lanes that store together: four blocks of 8 slots, two r
           const int kb = (lane & 3) | (dw << 2);  // block of 8 slots: cell * 2 + y
           const int r = lane >> 2;
           const uint32_t from = ring + (kb >> 1) * cell_bytes(D);
-          uint32_t w[4][kG];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) lds_words<kG>(from + v_word<D>(kb & 1, t, r, 0), w[t]);
-#pragma unroll
+#pragma unroll 1
           for (int g = 0; g < kG; ++g) {
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = lds32(from + v_word<D>(kb & 1, t, r, g));
             uint32_t s2[4], lo2[4];
             lds128(sb + L::kMetaV + (kb * kG + g) * 16, s2[0], s2[1], s2[2], s2[3]);
             lds128(sb + L::kVLo + (kb * kG + g) * 16, lo2[0], lo2[1], lo2[2], lo2[3]);
@@ -544,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               constexpr int kPair = decltype(pair)::value;
               const int c = 32 * g + 4 * r + kPair;
               sts128(dst + (kb >> 3) * L::kVChunk + c * 128 + (((kb & 7) ^ (c & 7)) << 4),
-                     expand<kPair>(w[0][g], s2[0], lo2[0]), expand<kPair>(w[1][g], s2[1], lo2[1]),
-                     expand<kPair>(w[2][g], s2[2], lo2[2]), expand<kPair>(w[3][g], s2[3], lo2[3]));
+                     expand<kPair>(w[0], s2[0], lo2[0]), expand<kPair>(w[1], s2[1], lo2[1]),
+                     expand<kPair>(w[2], s2[2], lo2[2]), expand<kPair>(w[3], s2[3], lo2[3]));
             };
             row(std::integral_constant<int, 0>{});
             row(std::integral_constant<int, 1>{});
@@ -553,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row(std::integral_constant<int, 3>{});
           }
           fence_proxy_async_smem();
-          mbar_arrive(bars.v_full(buf));
+          mbar_arrive(bars.v_full(slot2));
           mbar_arrive(bars.packed_empty(slot2));
         }
       });
@@ -661,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float x64[64];
           load_scores(half, x64);
@@ -689,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = ev - (m_used == -INFINITY ? 0.f : m_used);
         const uint64_t ct2 = f2pack(ct, ct), sub2 = f2pack(sub, sub);
         uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           float x64[64];
           load_scores(half, x64);
