@@ -327,6 +327,7 @@ class KVCache4:
         self.num_pages, self.heads, self.d, self.page_size = num_pages, heads, d, page_size
         self.dtype = dtype
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = self.data.device
         self._ws_bytes = {}  # of cache_forward, by (Hq, Nq, pages a table row)
         self._desc = FaCache(self.data.data_ptr(), num_pages, heads, page_size, d,
                              _DTYPES[dtype], 0)
@@ -336,37 +337,38 @@ def _ints(t, B, name, device):
     """Pointer of an int32 CUDA tensor [B] (contiguous) or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or t.shape[0] != B or \
+    if t.dtype != torch.int32 or t.device != device or t.shape != (B,) or \
             (B > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous int32 tensor [{B}] on {device}")
     return t.data_ptr()
 
 
-def _table(page_table, B, device):
+def _table(t, B, device):
     """(pointer, row stride, entries a row) of an int32 page table [B, pages]."""
-    if page_table.dtype != torch.int32 or page_table.device != device or \
-            page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1 or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != B or shape[1] < 1 or t.dtype != torch.int32 or \
+            t.device != device or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"page_table must be an int32 tensor [{B}, pages] on {device} with "
                          "contiguous rows")
-    return page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
+    return t.data_ptr(), stride[0], shape[1]
 
 
-def _cache_rows(fn, cache, k, v, page_table, start, counts):
-    ks = k.shape
-    if ks != v.shape or len(ks) != 4 or ks[1] != cache.heads or ks[3] != cache.d:
+def _cache_rows(fn, name, cache, k, v, page_table, start, counts):
+    shape = k.shape
+    if len(shape) != 4 or shape[1] != cache.heads or shape[3] != cache.d or v.shape != shape:
         raise ValueError(f"k and v must be [B, {cache.heads}, N, {cache.d}]")
-    dev = cache.data.device
+    dev = cache.device
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must be on the cache's device {dev}")
-    B, _, N, _ = ks
     if start is None:
         raise ValueError("start must be an int32 tensor [B]")
+    B = shape[0]
     table, stride, pages = _table(page_table, B, dev)
-    at, cnt = _ints(start, B, "start", dev), _ints(counts, B, "counts", dev)
-    _check(getattr(_lib_fast(), fn)(
-        cache._desc, _desc(k, "k"), _desc(v, "v"), table, stride, pages, at, cnt, B, N,
-        _stream(dev)), fn)
+    rc = fn(cache._desc, _desc(k, "k"), _desc(v, "v"), table, stride, pages,
+            _ints(start, B, "start", dev), _ints(counts, B, "counts", dev), B, shape[2],
+            _stream(dev))
+    if rc:
+        _check(rc, name)
 
 
 def cache_write(cache: KVCache4, k, v, page_table, start, counts=None):
@@ -380,7 +382,8 @@ def cache_write(cache: KVCache4, k, v, page_table, start, counts=None):
     These tensors are read on the device, so a captured graph follows them. A
     page or token out of range is skipped and reported by ``device_status``.
     """
-    _cache_rows("fa_cache_write", cache, k, v, page_table, start, counts)
+    _cache_rows(_lib_fast().fa_cache_write, "fa_cache_write", cache, k, v, page_table, start,
+                counts)
 
 
 def cache_read(cache: KVCache4, page_table, start, n: int, counts=None, k=None, v=None):
@@ -388,11 +391,13 @@ def cache_read(cache: KVCache4, page_table, start, n: int, counts=None, k=None, 
     to the cache's dtype; rows from ``counts[b]`` on are zeros. Arguments as
     for ``cache_write``; ``k`` and ``v`` receive the rows if given."""
     shape = (page_table.shape[0], cache.heads, n, cache.d)
-    k = torch.empty(shape, dtype=cache.dtype, device=cache.data.device) if k is None else k
-    v = torch.empty(shape, dtype=cache.dtype, device=cache.data.device) if v is None else v
+    if k is None:
+        k = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+    if v is None:
+        v = torch.empty_like(k)
     if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {list(shape)}")
-    _cache_rows("fa_cache_read", cache, k, v, page_table, start, counts)
+    _cache_rows(_lib_fast().fa_cache_read, "fa_cache_read", cache, k, v, page_table, start, counts)
     return k, v
 
 
@@ -417,22 +422,22 @@ def cache_forward(q, cache: KVCache4, page_table, lengths, causal: bool = False,
     qs = q.shape
     if len(qs) != 4 or qs[3] != cache.d or qs[1] % cache.heads:
         raise ValueError(f"q must be [B, Hq, Nq, {cache.d}] with Hq a multiple of {cache.heads}")
-    dev = cache.data.device
+    dev = cache.device
     B, Hq, Nq, d = qs
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if q.device != dev:
+        raise ValueError(f"q must be on the cache's device {dev}")
     if out is None:
         out = torch.empty_like(q) if o_dtype is None else torch.empty_like(q, dtype=o_dtype)
+    elif out.shape != qs or out.device != dev:
+        raise ValueError(f"out must be {list(qs)} on {dev}")
     if lse is None:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
-    if out.shape != qs or lse.shape != (B, Hq, Nq) or \
-            lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("out must be [B, Hq, Nq, d] and lse contiguous fp32 [B, Hq, Nq]")
-    if q.device != dev or out.device != dev or lse.device != dev:
-        raise ValueError(f"q, out and lse must be on the cache's device {dev}")
+    elif lse.shape != (B, Hq, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous() or \
+            lse.device != dev:
+        raise ValueError(f"lse must be contiguous fp32 {[B, Hq, Nq]} on {dev}")
     if lengths is None:
         raise ValueError("lengths must be an int32 tensor [B]")
     table, stride, pages = _table(page_table, B, dev)
-    ln, cnt = _ints(lengths, B, "lengths", dev), _ints(counts, B, "counts", dev)
     if workspace is None:
         nbytes = cache._ws_bytes.get((Hq, Nq, pages))
         if nbytes is None:
@@ -442,12 +447,15 @@ def cache_forward(q, cache: KVCache4, page_table, lengths, causal: bool = False,
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous, on the cache's device {dev}")
-    _check(_lib_fast().fa_cache_forward(
-        _desc(q, "q"), cache._desc, table, stride, pages, ln, cnt, _desc(out, "out"),
-        lse.data_ptr(), B, Hq, Nq, int(bool(causal)), scale,
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev)),
-        "fa_cache_forward")
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = _lib_fast().fa_cache_forward(
+        _desc(q, "q"), cache._desc, table, stride, pages, _ints(lengths, B, "lengths", dev),
+        _ints(counts, B, "counts", dev), _desc(out, "out"), lse.data_ptr(), B, Hq, Nq,
+        1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else float(scale),
+        workspace.data_ptr() if nbytes else None, nbytes, _stream(dev))
+    if rc:
+        _check(rc, "fa_cache_forward")
     return out, lse
 
 
