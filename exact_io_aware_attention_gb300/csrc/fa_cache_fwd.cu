@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
 // is one:  LSE = log sum_s 2^LSE_s,  O = sum_s 2^(LSE_s - LSE) O_s.
 // A thread holds 4 columns; kSub threads share a column's parts, each every
 // kSub-th, so that a chain over the whole GPU is a few loads deep.
-constexpr int kCombineThreads = 256, kCombineRows = 16;  // blocks of a segment at most
+constexpr int kCombineThreads = 256, kCombineRows = 32;  // blocks of a segment at most
 
 template <int D, int kRows, bool kF16>
 __global__ void __launch_bounds__(kCombineThreads)
