@@ -42,6 +42,14 @@
 // segment within one CTA's share is written out at once; parts of a segment go to scratch and
 // fa_cache_combine_kernel merges them in the order of the axis: the results
 // do not depend on timing.
+// Measured (GB300, ncu): 32 sequences of 1000 .. 16384 keys, 32 query heads on 8,
+// d = 128, bf16: 75.6 us for 357 MB (4.7 TB/s, 0.70 of the copy rate). The same
+// kernel without the arithmetic takes 62 us, without the copies 77 us at the time:
+// what bounds it is the issue of the expansion (0.57 instructions a cycle and
+// scheduler, the integer pipe, at half rate, 55 %). A warp more or less per
+// scheduler, two cells at a time, or the copies' number in flight change nothing;
+// fewer integer instructions do (groups in token pairs, lo through the tensor
+// cores: 87 -> 75 us). One sequence of 65536 keys, 16 heads: 36 us and the merge.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

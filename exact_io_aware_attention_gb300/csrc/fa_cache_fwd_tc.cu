@@ -41,6 +41,11 @@
 // would spread it to rows that do not see its token. So it enters V^ as 0,
 // and rows that see the token remember the group and put NaN in its channels
 // at the end. A NaN in K needs no such care: hidden scores are overwritten.
+// Measured (GB300): 2 sequences of 9000 and 16384 keys, 1024 new tokens each, 16
+// query heads on 4, d = 128: 243 us and the merge, 280 us in all (the kernel for few
+// rows: 1020 us), 0.76 PFLOP/s, the tensor pipe 39 % active. A tile of 128 keys for
+// 256 rows takes 2.2 us: two expansions of 1.4 us side by side, two softmaxes of
+// 1.4 us, all four sharing the schedulers (0.49 instructions a cycle each).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

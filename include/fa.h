@@ -368,8 +368,14 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
  * (all Nq). Query row i of sequence b, i < counts[b], is its token
  * lengths[b] - counts[b] + i (the new tokens, already written, are the last
  * ones); with causal it sees tokens up to itself, else all lengths[b]. A row
- * that sees no token, and rows from counts[b] on, get O = 0 and LSE = -inf.
- * B * Hq * Nq <= 2^30 - 1.
+ * that sees no token, and rows from counts[b] on, get O = 0 and LSE = -inf. A
+ * NaN among K or V reaches only the rows that see it (V: only its group's
+ * channels). B * Hq * Nq <= 2^30 - 1.
+ *
+ * Up to 64 query rows a cached head (Nq * Hq / heads; any number at d = 256)
+ * the codes are multiplied as they are and s, lo applied in fp32; the weights
+ * p s are rounded to f16. With more rows K, V and P are rounded to f16 operands
+ * (under a power of two for each tile of 128 keys). Sums are fp32 in both.
  *
  * The workspace (fa_cache_forward_workspace_bytes, 256-byte aligned; NULL
  * where that is 0) holds partial results while the call runs; calls that may

@@ -604,6 +604,64 @@ def test_bad_indices_are_skipped_and_reported():
     assert lib.fa_status_string(6) == b"FA_ERR_BAD_INDEX"
 
 
+@pytest.mark.parametrize("d,page,Hq", [(64, 16, 80), (128, 128, 70), (96, 256, 200)])
+def test_bad_pages_with_many_rows(d, page, Hq):
+    """A page outside the pool in the middle, found cell by cell or by the tile of 128 keys."""
+    L, n_pages = 700, -(-700 // page)
+    k, v, q = (rand((1, h, n, d), 120 + i, BF16) for i, (h, n) in enumerate(((1, L), (1, L), (Hq, 1))))
+    c = new_cache(n_pages, 1, d, page, BF16)
+    good = ints([list(range(n_pages))])
+    fa().cache_write(c, k.cuda(), v.cuda(), good, ints([0]))
+    assert status() == 0
+    bad = good.clone()
+    bad[0, 1] = n_pages + 7
+    for lengths in (L, L - 1):
+        o, lse = fa().cache_forward(q.cuda(), c, bad, ints([lengths]), o_dtype=torch.float32)
+        assert status() & BAD_INDEX == BAD_INDEX
+        seen = list(range(page)) + list(range(2 * page, lengths))
+        compare(o, lse, q, k[:, :, seen], v[:, :, seen], [len(seen)], None, False, None, "hidden")
+    bad[:] = -1
+    o, lse = fa().cache_forward(q.cuda(), c, bad, ints([L]), o_dtype=torch.float32)
+    assert status() & BAD_INDEX == BAD_INDEX
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_many_rows_from_pages_beyond_32_bit_offsets():
+    d, page = 128, 64
+    pool = (1 << 32) // (64 * 320) + 3
+    c = fa().KVCache4(pool, 1, d, page_size=page)
+    table = ints([[pool - 1, 3, pool - 2]])
+    k, v, q = (rand((1, h, 150, d), 130 + i, BF16) for i, h in enumerate((1, 1, 2)))
+    fa().cache_write(c, k.cuda(), v.cuda(), table, ints([0]))
+    o, lse = fa().cache_forward(q.cuda(), c, table, ints([150]), causal=True)
+    clean()
+    compare(o, lse, q, k, v, [150], None, True, None, "past 4 GiB, many rows")
+
+
+@pytest.mark.parametrize("Hq,Nq", [(2, 40), (3, 100)])
+def test_graph_of_many_rows_follows_lengths(Hq, Nq):
+    """A captured chunk replayed for shorter and longer sequences, down to none."""
+    d, page, pages = 64, 64, 40
+    L = 2000
+    k, v = rand((2, 1, L, d), 141, BF16), rand((2, 1, L, d), 142, BF16)
+    q = rand((2, Hq, Nq, d), 143, BF16)
+    table, pool = random_table(2, pages, seed=3)
+    table = table.cuda()
+    c = new_cache(pool, 1, d, page, BF16)
+    fa().cache_write(c, k.cuda(), v.cuda(), table, ints([0, 0]))
+    qq, lengths, counts = q.cuda(), ints([L, L]), ints([Nq, Nq])
+    fa().cache_forward(qq, c, table, lengths, causal=True, counts=counts)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = fa().cache_forward(qq, c, table, lengths, causal=True, counts=counts)
+    for ln, ct in (([L, 17], [Nq, 5]), ([0, 129], [0, Nq]), ([1999, 1000], [1, Nq])):
+        lengths.copy_(torch.tensor(ln))
+        counts.copy_(torch.tensor(ct))
+        graph.replay()
+        clean()
+        compare(o, lse, q, k, v, ln, ct, True, None, (ln, ct))
+
+
 @pytest.mark.parametrize("d,Nq", [(64, 1), (128, 9), (256, 1), (64, 40), (128, 100)])
 def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
     lib = binding.load_library()
