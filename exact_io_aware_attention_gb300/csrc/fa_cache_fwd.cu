@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
       // 16-bit steps of one slot, one after the other
       auto load_steps = [&](uint32_t from, float (&s)[kG]) {
         uint32_t w[kG / 2 + 1];
-        float unused;
         if constexpr (kG == 3) {  // begins with the high half of a word
+          float unused;
           w[0] = lds32(from - 2);
           w[1] = lds32(from + 2);
           unpack2<kF16>(w[0], unused, s[0]);
@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
         for (int y = 0; y < 2; ++y) lds_words<kG>(from + (4 * y + (r >> 1)) * (kG * 4), w[y]);
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-          float unused;
           if constexpr (kF16) {
+            float unused;
             unpack2<true>(__byte_perm(w[0][g], 0u, (r & 1) ? 0x4432 : 0x4410), a[g], unused);
             unpack2<true>(__byte_perm(w[1][g], 0u, (r & 1) ? 0x4432 : 0x4410), b2[g], unused);
           } else {
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
             l[nt][y] += pr[x2][nt][y] + pr[x2][nt][2 + y];
           }
         load_v(x2, cell);
-        float lo_a[kG], lo_b[kG];
+        [[maybe_unused]] float lo_a[kG], lo_b[kG];  // f16 only
         if constexpr (kF16) {
           load_own_token(cell + v_lo<D>(0, 0, 0), lo_a, lo_b);
           if constexpr (kMasked) {

@@ -81,7 +81,7 @@ struct TcLayout {
   static constexpr int kK = kQ + kNT * kQkBytes;          // (kNT = 1: the merge's O later)
   static constexpr int kV = kK + kKBufs * kQkBytes;       // two buffers
   static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
-  static constexpr int kMetaK = kRing + 2 * kPacked;      // [slot][g]: (s, s), (lo, lo) in f16
+  static constexpr int kMetaK = kRing + 2 * kPacked;      // [g][slot]: (s, s), (lo, lo) in f16
   static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
   static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][slot] groups of V that are NaN
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float down = pow2(-e);
 #pragma unroll
             for (int g = 0; g < kG; ++g)
-              sts64(sb + L::kMetaK + (dt * kG + g) * 8, pack_f16x2(s[g] * down, s[g] * down),
+              sts64(sb + L::kMetaK + (g * kKeys + dt) * 8, pack_f16x2(s[g] * down, s[g] * down),
                     pack_f16x2(lo[g] * down, lo[g] * down));
             if (dt == 0) scales[(i & 3) * 4] = pow2(e);
           }
@@ -462,8 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             code(kRoleExpand, 2)));
           if (!ok) break;
           const uint32_t dst = sb + L::kK + (i % L::kKBufs) * L::kQkBytes;
-          // eight lanes that store together: the four t, two slots four apart
-          const int t = lane & 3, low = (((lane >> 2) & 1) << 2) | (lane >> 3);
+          // eight lanes that load and store together: the four t, and two slots that
+          // differ in bit 0 (words of other banks) and in bit 2 (pieces of other banks)
+          const int t = lane & 3, low = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
 // (loops of the roles stay rolled: together they are more code than the
           // instruction cache holds; measured 12 % on a chunk of 1024 tokens)
 #pragma unroll 1
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               uint32_t s2, lo2;
-              lds64(sb + L::kMetaK + (slot * kG + g) * 8, s2, lo2);
+              lds64(sb + L::kMetaK + (g * kKeys + slot) * 8, s2, lo2);
               const int block = (g & 1) * 4 + t;
               sts128(dst + (g >> 1) * (kRows * 128) + slot * 128 + ((block ^ (slot & 7)) << 4),
                      expand<0>(w[g], s2, lo2), expand<1>(w[g], s2, lo2), expand<2>(w[g], s2, lo2),
@@ -549,7 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = lane >> 2;
           const uint32_t from = ring + (kb >> 1) * cell_bytes(D);
 #pragma unroll 1
-          for (int g = 0; g < kG; ++g) {
+          for (int gi = 0; gi < kG; ++gi) {
+            // (the four blocks of a warp lie 128-byte rows apart: at different groups
+            // their words are in different banks)
+            const int g = kG == 3 ? (gi + (lane & 3)) % 3 : (gi + (lane & 3)) & (kG - 1);
             uint32_t w[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) w[t] = lds32(from + v_word<D>(kb & 1, t, r, g));
