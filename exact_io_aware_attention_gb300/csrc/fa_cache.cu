@@ -86,26 +86,6 @@ __device__ __forceinline__ uint32_t round16(float x) {
   return pack2<kF16>(x, 0.f) & 0xffffu;
 }
 
-// Element-wise minimum of two pairs of 16-bit values, NaN if either is.
-template <bool kF16>
-__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if constexpr (kF16)
-    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else
-    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-template <bool kF16>
-__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if constexpr (kF16)
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // Four codes as the nibbles of 16 bits (exact in fp32), code 0 lowest.
 __device__ __forceinline__ uint32_t nibbles(float a, float b, float c, float d) {
   const float v = fmaf(fmaf(fmaf(d, 16.f, c), 16.f, b), 16.f, a);

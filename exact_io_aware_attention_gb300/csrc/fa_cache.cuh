@@ -182,7 +182,9 @@ cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows, cud
 // and 78 / 69 us (f16), 128 rows 98 / 74 us; 4 sequences of 4000 keys, 12 heads,
 // d = 64: 64 rows 40 / 49 us, 100 rows 57 / 53 us.
 constexpr int cache_forward_block_rows(int d, long long rows) {
-  return d == 256 || rows <= 8 ? 8 : rows <= 64 ? 16 : rows <= 128 ? 128 : 256;
+  return d == 256   ? (rows <= 64 ? 8 : 128)
+         : rows <= 8 ? 8
+                     : rows <= 64 ? 16 : rows <= 128 ? 128 : 256;
 }
 // CTAs that one SM holds (its registers and shared memory allow).
 constexpr int cache_forward_ctas_per_sm(int d, int block_rows) {

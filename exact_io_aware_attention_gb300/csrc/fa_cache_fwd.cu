@@ -946,19 +946,21 @@ cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
                     kMinShare;
   if (shares < (double)p.ctas) p.ctas = (int)shares + 1;
   cudaError_t e;
-  if constexpr (D <= 128) {
-    e = rows >= 128  ? launch_cache_forward_tc(p, rows, stream)
-        : rows == 16 ? launch_d<D, 2, kF16>(p, stream)
-                     : launch_d<D, 1, kF16>(p, stream);
-    if (e != cudaSuccess || p.whole) return e;
-    return rows == 256   ? launch_combine<D, 256, kF16>(p, stream)
-           : rows == 128 ? launch_combine<D, 128, kF16>(p, stream)
-           : rows == 16 ? launch_combine<D, 16, kF16>(p, stream)
-                        : launch_combine<D, 8, kF16>(p, stream);
-  } else {
+  if (rows >= 128)
+    e = launch_cache_forward_tc(p, rows, stream);
+  else if constexpr (D == 256)
     e = launch_d<D, 1, kF16>(p, stream);
-    return e != cudaSuccess || p.whole ? e : launch_combine<D, 8, kF16>(p, stream);
+  else
+    e = rows == 16 ? launch_d<D, 2, kF16>(p, stream) : launch_d<D, 1, kF16>(p, stream);
+  if (e != cudaSuccess || p.whole) return e;
+  switch (rows) {
+    case 8: return launch_combine<D, 8, kF16>(p, stream);
+    case 128: return launch_combine<D, 128, kF16>(p, stream);
   }
+  if constexpr (D != 256)
+    return rows == 16 ? launch_combine<D, 16, kF16>(p, stream)
+                      : launch_combine<D, 256, kF16>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

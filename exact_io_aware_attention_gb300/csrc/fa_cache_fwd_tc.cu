@@ -61,33 +61,38 @@ constexpr int kThreads = 640;
 constexpr int kRegsLaunch = 96, kRegsIssue = 48, kRegsSoftmax = 128, kRegsExpand = 88;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand == 5 * kRegsLaunch, "register split");
 static_assert(kRegsLaunch * kThreads <= 65536, "registers of an SM");
-constexpr int kRows = 128, kKeys = 128, kTileCells = kKeys / kCellTokens;
+constexpr int kRows = 128;
+// Keys of a tile: with d = 256, twice as many would not fit the shared memory.
+constexpr int tile_keys(int d) { return d == 256 ? 64 : 128; }
 constexpr float kRescaleThreshold = 8.0f;  // log2: m moves when P would pass 2^8
 
 template <int D, int kNT>
 struct TcLayout {
   static constexpr int kG = D / 32;
-  static constexpr int kChunks = (D + 63) / 64;           // 64-channel chunks of a Q or K row
-  static constexpr int kQkBytes = kChunks * kRows * 128;  // 128 rows of 128 bytes a chunk
-  static constexpr int kVChunk = D * 128;                 // D rows of 64 slots
-  static constexpr int kVBytes = 2 * kVChunk;
-  static constexpr int kPacked = kTileCells * cell_bytes(D);
+  static constexpr int kKeys = tile_keys(D);
+  static constexpr int kChunks = (D + 63) / 64;         // 64-channel chunks of a Q or K row
+  static constexpr int kQBytes = kChunks * kRows * 128;  // 128 rows of 128 bytes a chunk
+  static constexpr int kKBytes = kChunks * kKeys * 128;
+  static constexpr int kVChunk = D * 128;               // D rows of 64 slots
+  static constexpr int kVBytes = kKeys / 64 * kVChunk;
+  static constexpr int kPacked = kKeys / kCellTokens * cell_bytes(D);
   static constexpr int kQ = 0;
   // Buffers of K and V tiles: with 256 rows there is room for three. K's is free
   // as soon as both S have been issued, V's only after both P V, a step later
   // (measured with one of V and two of K: 2.5 us a tile, the expansion of V waiting
   // for the products and they for it).
-  static constexpr int kKBufs = kNT == 2 ? 1 : 2;
-  static constexpr int kK = kQ + kNT * kQkBytes;          // (kNT = 1: the merge's O later)
-  static constexpr int kV = kK + kKBufs * kQkBytes;       // two buffers
+  static constexpr int kKBufs = kNT == 2 || D == 256 ? 1 : 2;
+  static constexpr int kK = kQ + kNT * kQBytes;           // (kNT = 1: the merge's O later)
+  static constexpr int kV = kK + kKBufs * kKBytes;        // two buffers
   static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
   static constexpr int kMetaK = kRing + 2 * kPacked;      // [g][slot]: (s, s), (lo, lo) in f16
   static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
-  static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][slot] groups of V that are NaN
-  static constexpr int kScales = kNan + 4 * kKeys;        // [4]: 2^eK, 2^eV, 2^-eV, eV
+  static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][128] groups of V that are NaN
+  static constexpr int kScales = kNan + 4 * 128;          // [4]: 2^eK, 2^eV, 2^-eV, eV
   static constexpr int kFlags = kScales + 4 * 16;         // [4] any NaN, [4] found cells, reductions
-  static constexpr int kBars = kFlags + 32 + 48;
+  static constexpr int kRowScale = kFlags + 32 + 48;      // [128] of the query rows (turns)
+  static constexpr int kBars = kRowScale + 4 * kRows;
   static constexpr int kNumBars = 22;
   static constexpr int kTmem = kBars + kNumBars * 8;
   static constexpr int kMisc = (kTmem + 8 + 15) / 16 * 16;
@@ -130,6 +135,14 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   st_shared_v4(a, x, y, z, w);
+}
+// Copies 16 bytes (`bytes` = 0: writes zeros), without waiting.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
@@ -189,7 +202,11 @@ template <int D, bool kF16, int kNT>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_fwd_tc_kernel(const __grid_constant__ CacheFwdParams p) {
   using L = TcLayout<D, kNT>;
-  constexpr int kG = L::kG;
+  constexpr int kG = L::kG, kKeys = L::kKeys, kTileCells = kKeys / kCellTokens;
+  constexpr int kSCols = 128;           // tensor memory columns of S
+  constexpr bool kTurns = kNT == 1 && D != 256;  // the softmax warpgroups take turns at the tiles
+  // the threads of an expansion hold the groups of a slot, or parts of them
+  constexpr int kParts = 128 / kKeys, kGp = kG / kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *const smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -246,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (mine.found && f < mine.f_end) {
       const Piece piece(p, blocks, misc, f, mine.f_end);
       if (piece.h < 0 || piece.h >= heads) break;
-      const int count =
-          max(0, min(piece.t1, (piece.cells + kTileCells - 1) / kTileCells) - piece.t0);
+      constexpr int kPerUnit = kUnitTokens / kKeys;
+      const int count = max(0, min(piece.t1 * kPerUnit, (piece.cells + kTileCells - 1) / kTileCells) -
+                                   piece.t0 * kPerUnit);
       work(piece, count, tile0, pieces);
       tc_fence_before();
       __syncthreads();
@@ -266,13 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     setmaxnreg_dec<kRegsIssue>();
     walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t pieces) {
-      const int cells = piece.cells;
+      const int cells = piece.cells, cell0 = piece.t0 * (kUnitTokens / kCellTokens);
     if (warp == 0) {
       // ---- copies ----------------------------------------------------------
       const int32_t *const table = p.pool.table + (size_t)((long long)piece.b * p.pool.table_stride);
       const bool one_copy = p.pool.page_cells % kTileCells == 0;
       auto page_of = [&](int k) {  // of this lane's cell of tile k
-        const int c = (piece.t0 + k) * kTileCells + lane;
+        const int c = cell0 + k * kTileCells + lane;
         return lane < kTileCells && k < count && c < cells ? table[p.pool.by_page_cells.div(c)] : -1;
       };
       int page = page_of(0);
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.packed_empty(slot), ((i >> 1) & 1) ^ 1, st,
                                                    code(kRoleLoad, 1)));
         if (!ok || (p.debug_flags & kDebugSkipLoads)) break;
-        const int c = (piece.t0 + issued) * kTileCells + lane;
+        const int c = cell0 + issued * kTileCells + lane;
         const bool wanted = lane < kTileCells && c < cells;
         const bool here = wanted && p.pool.page_ok(page);
         if (wanted && !here) atomicCAS(p.status, 0u, index_code(kKernCacheFwd, 2));
@@ -321,12 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
         const uint64_t v_desc = sdesc_sw128(sb + L::kV, 16, 1024);
         auto issue_s = [&](int t, uint32_t i) {
-          const uint64_t q = q_desc + (kNT == 2 ? t : 0) * (L::kQkBytes >> 4);
-          const uint64_t k = k_desc + (i % L::kKBufs) * (L::kQkBytes >> 4);
+          const uint64_t q = q_desc + (kNT == 2 ? t : 0) * (L::kQBytes >> 4);
+          const uint64_t k = k_desc + (i % L::kKBufs) * (L::kKBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const int off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
-            mma_f16kind_ss(tmem + t * kKeys, q + off, k + off, kIdS, kk > 0);
+            const int q_off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+            const int k_off = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
+            mma_f16kind_ss(tmem + t * kSCols, q + q_off, k + k_off, kIdS, kk > 0);
           }
           mma_commit(bars.s_full(t));
         };
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t v = v_desc + (i & 1) * (L::kVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kKeys + kk * 8,
+            mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kSCols + kk * 8,
                            v + (((kk >> 2) * L::kVChunk + (kk & 3) * 32) >> 4), kIdPV,
                            (!first || kk > 0) ? 1u : 0u);
           mma_commit(bars.pv_done(t));
@@ -346,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return here;
         };
         bool ok = mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleMma, 1)) && k_here(tile0);
-        if constexpr (kNT == 2) {
+        if constexpr (!kTurns) {
           if (ok) {
             issue_s(0, tile0);
             if (two) issue_s(1, tile0);
@@ -420,30 +439,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
           {
-            // s and lo of slot dt
-            const int cell = dt >> 4;
-            const uint32_t at = ring + cell * cell_bytes(D) + k_lo<D>(dt & 15, 0);
-            float s[kG], lo[kG];
-            uint32_t w[kG];  // kG lo, then kG s, in pairs
+            // s and lo of a slot's groups g0 .. g0 + kGp - 1
+            const int own = dt % kKeys, g0 = dt / kKeys * kGp, cell = own >> 4;
+            const uint32_t at = ring + cell * cell_bytes(D) + k_lo<D>(own & 15, g0);
+            float s[kGp], lo[kGp];
+            uint32_t w[kGp];  // kGp lo, then kGp s, in pairs
             if constexpr (kG == 3) {
               lds_words<3>(at, w);
               unpack2<kF16>(w[0], lo[0], lo[1]);
               unpack2<kF16>(w[1], lo[2], s[0]);
               unpack2<kF16>(w[2], s[1], s[2]);
             } else {
-              lds_words<kG>(at, w);
+              if constexpr (kParts == 1) {
+                lds_words<kGp>(at, w);
+              } else {
+                lds_words<kGp / 2>(at, w);
+                lds_words<kGp / 2>(at + D / 16, w + kGp / 2);
+              }
 #pragma unroll
-              for (int x = 0; x < kG / 2; ++x) {
+              for (int x = 0; x < kGp / 2; ++x) {
                 unpack2<kF16>(w[x], lo[2 * x], lo[2 * x + 1]);
-                unpack2<kF16>(w[kG / 2 + x], s[2 * x], s[2 * x + 1]);
+                unpack2<kF16>(w[kGp / 2 + x], s[2 * x], s[2 * x + 1]);
               }
             }
             const bool live = ((found >> cell) & 1) &&
-                              (piece.t0 + k) * kKeys + cell * kCellTokens + cell_token(dt & 15) <
+                              piece.t0 * kUnitTokens + k * kKeys + cell * kCellTokens +
+                                      cell_token(own & 15) <
                                   piece.vis;
             float top = 0.f;
 #pragma unroll
-            for (int g = 0; g < kG; ++g) {
+            for (int g = 0; g < kGp; ++g) {
               if (!live) s[g] = lo[g] = 0.f;
               // (a NaN does not enter the maximum)
               top = fmaxf(top, fmaxf(fabsf(lo[g]), fabsf(fmaf(15.f, s[g], lo[g]))));
@@ -451,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = tile_exponent(expand_max<1>(top, red, dw));
             const float down = pow2(-e);
 #pragma unroll
-            for (int g = 0; g < kG; ++g)
-              sts64(sb + L::kMetaK + (g * kKeys + dt) * 8, pack_f16x2(s[g] * down, s[g] * down),
+            for (int g = 0; g < kGp; ++g)
+              sts64(sb + L::kMetaK + ((g0 + g) * kKeys + own) * 8, pack_f16x2(s[g] * down, s[g] * down),
                     pack_f16x2(lo[g] * down, lo[g] * down));
             if (dt == 0) scales[(i & 3) * 4] = pow2(e);
           }
@@ -461,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_wait_inl(bars.k_free(i % L::kKBufs), ((i / L::kKBufs) & 1) ^ 1, st,
                             code(kRoleExpand, 2)));
           if (!ok) break;
-          const uint32_t dst = sb + L::kK + (i % L::kKBufs) * L::kQkBytes;
+          const uint32_t dst = sb + L::kK + (i % L::kKBufs) * L::kKBytes;
           // eight lanes that load and store together: the four t, and two slots that
           // differ in bit 0 (words of other banks) and in bit 2 (pieces of other banks)
           const int t = lane & 3, low = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
@@ -469,17 +494,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           // instruction cache holds; measured 12 % on a chunk of 1024 tokens)
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
-            const int slot = (dw * 4 + x) * 8 + low;
-            uint32_t w[kG];
-            lds_words<kG>(ring + (slot >> 4) * cell_bytes(D) + k_word<D>(slot & 15, t, 0), w);
+            constexpr int kEights = kKeys / 32;  // of slots a warp
+            const int slot = (dw * kEights + x % kEights) * 8 + low, g0 = x / kEights * kGp;
+            uint32_t w[kGp];
+            lds_words<kGp>(ring + (slot >> 4) * cell_bytes(D) + k_word<D>(slot & 15, t, g0), w);
 #pragma unroll
-            for (int g = 0; g < kG; ++g) {
+            for (int y = 0; y < kGp; ++y) {
+              const int g = g0 + y;
               uint32_t s2, lo2;
               lds64(sb + L::kMetaK + (g * kKeys + slot) * 8, s2, lo2);
               const int block = (g & 1) * 4 + t;
-              sts128(dst + (g >> 1) * (kRows * 128) + slot * 128 + ((block ^ (slot & 7)) << 4),
-                     expand<0>(w[g], s2, lo2), expand<1>(w[g], s2, lo2), expand<2>(w[g], s2, lo2),
-                     expand<3>(w[g], s2, lo2));
+              sts128(dst + (g >> 1) * (kKeys * 128) + slot * 128 + ((block ^ (slot & 7)) << 4),
+                     expand<0>(w[y], s2, lo2), expand<1>(w[y], s2, lo2), expand<2>(w[y], s2, lo2),
+                     expand<3>(w[y], s2, lo2));
             }
           }
           fence_proxy_async_smem();
@@ -504,19 +531,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
           {
-            // s and lo of one token: half z of pair (cell, y, t)
-            const int cell = dt >> 4, y = (dt >> 3) & 1, t = (dt >> 1) & 3, z = dt & 1;
+            // s and lo of groups g0 .. of one token: half z of pair (cell, y, t)
+            const int own = dt % kKeys, part = dt / kKeys, g0 = part * kGp;
+            const int cell = own >> 4, y = (own >> 3) & 1, t = (own >> 1) & 3, z = own & 1;
             const uint32_t at = ring + cell * cell_bytes(D);
             const int token = t + 8 * y + 4 * z;
             const bool live = ((found >> cell) & 1) &&
-                              (piece.t0 + k) * kKeys + cell * kCellTokens + token < piece.vis;
-            uint32_t ws[kG], wl[kG];
-            lds_words<kG>(at + v_s<D>(y, t, 0), ws);
-            lds_words<kG>(at + v_lo<D>(y, t, 0), wl);
-            float s[kG], lo[kG], top = 0.f;
+                              piece.t0 * kUnitTokens + k * kKeys + cell * kCellTokens + token <
+                                  piece.vis;
+            uint32_t ws[kGp], wl[kGp];
+            lds_words<kGp>(at + v_s<D>(y, t, g0), ws);
+            lds_words<kGp>(at + v_lo<D>(y, t, g0), wl);
+            float s[kGp], lo[kGp], top = 0.f;
             uint32_t nans = 0;
 #pragma unroll
-            for (int g = 0; g < kG; ++g) {
+            for (int g = 0; g < kGp; ++g) {
               unpack2<kF16>(__byte_perm(ws[g], wl[g], z ? 0x7632 : 0x5410), s[g], lo[g]);
               if (!live) s[g] = lo[g] = 0.f;
               if (!(lo[g] == lo[g])) {
@@ -530,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = tile_exponent(expand_max<2>(top, red + 4, dw));
             const float down = pow2(-e);
 #pragma unroll
-            for (int g = 0; g < kG; ++g) {
-              const uint32_t o = ((((cell * 2 + y) * kG + g) * 4 + t) * 2 + z) * 2;
+            for (int g = 0; g < kGp; ++g) {
+              const uint32_t o = ((((cell * 2 + y) * kG + g0 + g) * 4 + t) * 2 + z) * 2;
               sts16(sb + L::kMetaV + o, pack_f16x2(s[g] * down, 0.f));
               sts16(sb + L::kVLo + o, pack_f16x2(lo[g] * down, 0.f));
             }
-            smem[L::kNan + (i & 3) * kKeys + cell * 16 + cell_slot(token)] = (uint8_t)nans;
+            smem[L::kNan + (i & 3) * 128 + part * kKeys + cell * 16 + cell_slot(token)] = (uint8_t)nans;
             if (dt == 0) {
               nan_flag[i & 3] = red[8] + red[9] + red[10] + red[11] > 0.f;
               scales[(i & 3) * 4 + 1] = down;
@@ -546,14 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           expand_sync<2>(true);
           const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
           // eight lanes that store together: four blocks of 8 slots, two r
-          const int kb = (lane & 3) | (dw << 2);  // block of 8 slots: cell * 2 + y
+          const int kb = (lane & 3) | (dw % (kKeys / 32) << 2);  // block of 8 slots: cell * 2 + y
+          const int g0 = dw / (kKeys / 32) * kGp;
           const int r = lane >> 2;
           const uint32_t from = ring + (kb >> 1) * cell_bytes(D);
 #pragma unroll 1
-          for (int gi = 0; gi < kG; ++gi) {
+          for (int gi = 0; gi < kGp; ++gi) {
             // (the four blocks of a warp lie 128-byte rows apart: at different groups
             // their words are in different banks)
-            const int g = kG == 3 ? (gi + (lane & 3)) % 3 : (gi + (lane & 3)) & (kG - 1);
+            const int g =
+                g0 + (kGp == 3 ? (gi + (lane & 3)) % 3 : (gi + (lane & 3)) & (kGp - 1));
             uint32_t w[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) w[t] = lds32(from + v_word<D>(kb & 1, t, r, g));
@@ -590,65 +621,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = p.by_group.div(row), hq = piece.h * p.group + (row - tok * p.group);
       const bool live = tok < n;
       const bool warp_live = p.by_group.div(tile_row0 + (warp & 3) * 32) < n;  // its first row's token
-      const bool has_rows = kNT == 1 || t == 0 || tile_row0 < p.nq * p.group;
+      const bool has_rows = kTurns || t == 0 || (kNT == 2 && tile_row0 < p.nq * p.group);
+      // The row scaled by a power of two, its largest element below 2^11. A thread
+      // copies its own row to where the product reads it and scales it there: all
+      // of it is on its way at once, in little code (code that runs once a piece
+      // costs most in fetching it).
       float c_row = 0.f;
-      {
-        // the row scaled by a power of two, its largest element below 2^11
+      float *const row_scale = reinterpret_cast<float *>(smem + L::kRowScale);
+      if (kNT == 2 || t == 0) {
         const uint16_t *const src = static_cast<const uint16_t *>(p.q) +
                                     (live ? p.sq.row(piece.b, hq, tok) : (size_t)0);
-        float big = 0.f;
-        bool finite = true;
-#pragma unroll
+        const uint32_t own = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQBytes + r * 128;
+        auto at = [&](int x) {
+          return own + (x >> 3) * (kRows * 128) + (((x & 7) ^ (r & 7)) << 4);
+        };
+#pragma unroll 4
+        for (int x = 0; x < D / 8; ++x) cp_async16(at(x), src + x * 8, live ? 16 : 0);
+        cp_async_wait_all();
+        uint32_t top2 = 0;  // the largest magnitudes of the even and the odd channels
+#pragma unroll 4
         for (int x = 0; x < D / 8; ++x) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live) w = *reinterpret_cast<const uint4 *>(src + x * 8);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          uint32_t w[4];
+          lds128(at(x), w[0], w[1], w[2], w[3]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float a, b;
-            unpack2<kF16>(in[y], a, b);
-            big = fmaxf(big, fmaxf(fabsf(a), fabsf(b)));
-            finite = finite && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
-          }
+          for (int y = 0; y < 4; ++y) top2 = max2_nan<kF16>(top2, w[y] & 0x7fff7fffu);
         }
+        float big, big1;
+        unpack2<kF16>(top2, big, big1);
+        const bool finite = big < INFINITY && big1 < INFINITY;
+        big = fmaxf(big, big1);
         const int e = max((int)(__float_as_uint(big) >> 23), 40);
         const bool scaled = big > 0.f && finite;
         // (a row with an infinity or a NaN is NaN throughout: so are its scores)
-        const float up = !finite ? __uint_as_float(0x7fffffffu)
-                         : scaled ? __uint_as_float((uint32_t)(264 - e) << 23)
-                                  : 1.f;
+        const float up = scaled ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
         c_row = (scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f) * p.scale_log2;
-#pragma unroll
+#pragma unroll 2
         for (int x = 0; x < D / 8; ++x) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live) w = *reinterpret_cast<const uint4 *>(src + x * 8);
+          uint32_t w[4];
+          lds128(at(x), w[0], w[1], w[2], w[3]);
           float q[8];
-          unpack2<kF16>(w.x, q[0], q[1]);
-          unpack2<kF16>(w.y, q[2], q[3]);
-          unpack2<kF16>(w.z, q[4], q[5]);
-          unpack2<kF16>(w.w, q[6], q[7]);
-          if (!finite)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) q[y] = 1.f;
-          if (kNT == 2 || t == 0)
-            sts128(sb + L::kQ + (kNT == 2 ? t : 0) * L::kQkBytes + (x >> 3) * (kRows * 128) +
-                       r * 128 + (((x & 7) ^ (r & 7)) << 4),
-                   pack_f16x2(q[0] * up, q[4] * up), pack_f16x2(q[1] * up, q[5] * up),
-                   pack_f16x2(q[2] * up, q[6] * up), pack_f16x2(q[3] * up, q[7] * up));
+          for (int y = 0; y < 4; ++y) unpack2<kF16>(w[y], q[2 * y], q[2 * y + 1]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            w[y] = pack_f16x2(q[y] * up, q[y + 4] * up);
+            if (!finite) w[y] = 0x7fff7fffu;
+          }
+          sts128(at(x), w[0], w[1], w[2], w[3]);
         }
+        if (kTurns) row_scale[r] = c_row;
         fence_proxy_async_smem();
-        if (kNT == 2 || t == 0) mbar_arrive(bars.q_full());
+        mbar_arrive(bars.q_full());
+      }
+      bool ok = true;
+      if (kTurns && t == 1) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_inl(bars.q_full(), pieces & 1, st, code(kRoleSoftmax, 6)));
+        c_row = row_scale[r];
       }
       const int lim = p.causal && live ? len - n + tok + 1 : len;
       const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
-      const uint32_t tS = lanes + t * kKeys, tO = lanes + 256 + t * D;
+      const uint32_t tS = lanes + t * kSCols, tO = lanes + 256 + t * D;
       float m_used = -INFINITY, l = 0.f;
       uint32_t nan_groups = 0;
-      bool ok = true;
       bool any = false;
-      for (int k = kNT == 1 ? ((tile0 ^ t) & 1) : 0; k < count && has_rows; k += kNT == 1 ? 2 : 1) {
+      for (int k = kTurns ? ((tile0 ^ t) & 1) : 0; k < count && has_rows && ok; k += kTurns ? 2 : 1) {
         const uint32_t i = tile0 + k;
-        const uint32_t parity = (kNT == 1 ? i >> 1 : i) & 1;
+        const uint32_t parity = (kTurns ? i >> 1 : i) & 1;
         ok = __all_sync(0xffffffffu,
                         mbar_wait_inl(bars.s_full(t), parity, st, code(kRoleSoftmax, 1)));
         if (!ok) break;
@@ -660,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ct = c_row * scales[(i & 3) * 4];
         const uint32_t found = (uint32_t)found_cells[i & 3];
-        const int key0 = (piece.t0 + k) * kKeys;
-        const bool masked = key0 + kKeys > all || found != 0xffu;
+        const int key0 = piece.t0 * kUnitTokens + k * kKeys;
+        const bool masked = key0 + kKeys > all || found != (1u << kTileCells) - 1;
         const int left = min(lim, vis) - key0;
         // scores of keys 64 half .. 64 half + 63 (slots), hidden ones -inf
         auto load_scores = [&](int half, float (&x64)[64]) {
@@ -682,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < kKeys / 64; ++half) {
           float x64[64];
           load_scores(half, x64);
 #pragma unroll
@@ -695,9 +734,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const float fv = scales[(i & 3) * 4 + 1], ev = scales[(i & 3) * 4 + 2];
         if (nan_flag[i & 3])
-          for (int x = 0; x < kKeys; ++x)
-            if ((x & ~15) + cell_token(x & 15) < left)
-              nan_groups |= smem[L::kNan + (i & 3) * kKeys + x];
+          for (int x = 0; x < 128; ++x)
+            if ((x % kKeys & ~15) + cell_token(x & 15) < left)
+              nan_groups |= (uint32_t)smem[L::kNan + (i & 3) * 128 + x] << (x / kKeys * kGp);
         const float m_tile = fmaf(fmax3(mp[0], mp[1], fmaxf(mp[2], mp[3])), ct, ev);
         const bool need = m_tile > m_used + kRescaleThreshold;
         float alpha = 1.f;
@@ -710,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ct2 = f2pack(ct, ct), sub2 = f2pack(sub, sub);
         uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < kKeys / 64; ++half) {
           float x64[64];
           load_scores(half, x64);
           uint32_t pk[32];
@@ -731,14 +770,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any && __any_sync(0xffffffffu, need)) {
           // O *= alpha: P V of this t's previous tile is in it, having been issued
           // before this tile's S
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t o[16];
-            tmem_ld16(tO + q * 16, o);
+#pragma unroll 1
+          for (int q = 0; q < kG; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + q * 32, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-            tmem_st16(tO + q * 16, o);
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+            tmem_st32(tO + q * 32, o);
           }
         }
         tmem_wait_st();
@@ -748,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       // ---- O / l and the log-sum-exp -------------------------------------------
-      if constexpr (kNT == 2) {
+      if constexpr (!kTurns) {
         if (ok && any)
           ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(t), (tile0 + count - 1) & 1, st,
                                                      code(kRoleSoftmax, 2)));
@@ -769,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           stat[kRows + r] = l;
           stat[2 * kRows + r] = __uint_as_float(nan_groups);
           if (any && warp_live) {
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
               uint32_t o[16];
               tmem_ld16(tO + q * 16, o);
@@ -791,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w1 = top == m1 ? 1.f : ex2_approx(m1 - top);
           const bool other = count > 1 || !any;  // t = 1 had a tile
           if (other) {
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
               uint32_t o[16];
               tmem_ld16(tO + q * 16, o);
@@ -823,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool store = tok < p.nq;  // (nothing reads the other rows)
         const size_t at = store && whole ? p.so.row(piece.b, hq, tok) : 0;
         float *const to32 = whole ? static_cast<float *>(p.o) + at : p.part + prow * D;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < kG; ++q) {
           uint32_t o[32];
           if (count > 0) {
@@ -886,7 +925,9 @@ cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
 
 template <int D, bool kF16>
 cudaError_t launch_tc_rows(const CacheFwdParams &p, bool two, cudaStream_t stream) {
-  return two ? launch_tc<D, kF16, 2>(p, stream) : launch_tc<D, kF16, 1>(p, stream);
+  if constexpr (D != 256)
+    if (two) return launch_tc<D, kF16, 2>(p, stream);
+  return launch_tc<D, kF16, 1>(p, stream);
 }
 
 }  // namespace
@@ -898,6 +939,7 @@ cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows,
     case 64: return f16 ? launch_tc_rows<64, true>(p, two, stream) : launch_tc_rows<64, false>(p, two, stream);
     case 96: return f16 ? launch_tc_rows<96, true>(p, two, stream) : launch_tc_rows<96, false>(p, two, stream);
     case 128: return f16 ? launch_tc_rows<128, true>(p, two, stream) : launch_tc_rows<128, false>(p, two, stream);
+    case 256: return f16 ? launch_tc_rows<256, true>(p, two, stream) : launch_tc_rows<256, false>(p, two, stream);
     default: return cudaErrorInvalidValue;
   }
 }

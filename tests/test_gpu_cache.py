@@ -229,7 +229,7 @@ def test_chunks_of_a_prompt(d, Nq, Hq, Hk):
     attend_case(2, Hq, Hk, Nq, [Nq + 77, Nq], d, 32, F16, True, counts=[Nq - 5, Nq], what="chunk f16")
 
 
-@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("B,Hq,Hk,Nq,lengths,page,counts", [
     (1, 65, 1, 1, [1], 16, None),                       # one token, 65 heads on one
@@ -253,6 +253,7 @@ def test_sizes_of_values(v_scale, k_scale):
     """V far from 1 (the weights p s must keep their bits), sharp and flat scores."""
     attend_case(2, 4, 2, 2, [333, 40], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
     attend_case(1, 40, 1, 2, [333], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
+    attend_case(1, 40, 1, 2, [333], 256, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
     if 1e-4 < v_scale < 1e3 and k_scale > 1e-4:
         attend_case(2, 4, 2, 2, [333, 40], 64, 32, F16, True, v_scale=v_scale, k_scale=k_scale)
 
@@ -318,7 +319,7 @@ def test_strided_queries_and_outputs():
 
 
 @pytest.mark.parametrize("d,Hq", [(64, 2), (96, 2), (128, 2), (256, 2), (64, 17), (96, 20),
-                                  (128, 36)])
+                                  (128, 36), (256, 20)])
 def test_non_finite_values_stay_where_they_are_seen(d, Hq):
     """NaN and infinities in a key or value reach only the rows that see it, and only its
     group's outputs where it is a value; a NaN query spoils its own row alone."""
@@ -604,9 +605,10 @@ def test_bad_indices_are_skipped_and_reported():
     assert lib.fa_status_string(6) == b"FA_ERR_BAD_INDEX"
 
 
-@pytest.mark.parametrize("d,page,Hq", [(64, 16, 80), (128, 128, 70), (96, 256, 200)])
+@pytest.mark.parametrize("d,page,Hq", [(64, 16, 80), (128, 128, 70), (96, 256, 200), (256, 48, 30),
+                                       (256, 128, 90)])
 def test_bad_pages_with_many_rows(d, page, Hq):
-    """A page outside the pool in the middle, found cell by cell or by the tile of 128 keys."""
+    """A page outside the pool in the middle, found cell by cell or by the tile of keys."""
     L, n_pages = 700, -(-700 // page)
     k, v, q = (rand((1, h, n, d), 120 + i, BF16) for i, (h, n) in enumerate(((1, L), (1, L), (Hq, 1))))
     c = new_cache(n_pages, 1, d, page, BF16)
@@ -626,9 +628,10 @@ def test_bad_pages_with_many_rows(d, page, Hq):
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
-def test_many_rows_from_pages_beyond_32_bit_offsets():
-    d, page = 128, 64
-    pool = (1 << 32) // (64 * 320) + 3
+@pytest.mark.parametrize("d", [128, 256])
+def test_many_rows_from_pages_beyond_32_bit_offsets(d):
+    page = 64
+    pool = (1 << 32) // (64 * 5 * d // 2) + 3
     c = fa().KVCache4(pool, 1, d, page_size=page)
     table = ints([[pool - 1, 3, pool - 2]])
     k, v, q = (rand((1, h, 150, d), 130 + i, BF16) for i, h in enumerate((1, 1, 2)))
@@ -638,10 +641,10 @@ def test_many_rows_from_pages_beyond_32_bit_offsets():
     compare(o, lse, q, k, v, [150], None, True, None, "past 4 GiB, many rows")
 
 
-@pytest.mark.parametrize("Hq,Nq", [(2, 40), (3, 100)])
-def test_graph_of_many_rows_follows_lengths(Hq, Nq):
+@pytest.mark.parametrize("Hq,Nq,d", [(2, 40, 64), (3, 100, 64), (1, 100, 256)])
+def test_graph_of_many_rows_follows_lengths(Hq, Nq, d):
     """A captured chunk replayed for shorter and longer sequences, down to none."""
-    d, page, pages = 64, 64, 40
+    page, pages = 64, 40
     L = 2000
     k, v = rand((2, 1, L, d), 141, BF16), rand((2, 1, L, d), 142, BF16)
     q = rand((2, Hq, Nq, d), 143, BF16)
@@ -662,7 +665,8 @@ def test_graph_of_many_rows_follows_lengths(Hq, Nq):
         compare(o, lse, q, k, v, ln, ct, True, None, (ln, ct))
 
 
-@pytest.mark.parametrize("d,Nq", [(64, 1), (128, 9), (256, 1), (64, 40), (128, 100)])
+@pytest.mark.parametrize("d,Nq", [(64, 1), (128, 9), (256, 1), (64, 40), (128, 100),
+                                  (256, 20), (256, 40)])
 def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
     lib = binding.load_library()
     c, table, q, k, v = attend_case(1, 2, 1, Nq, [500], d, 64, BF16, True)
@@ -670,7 +674,7 @@ def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
         assert lib.fa_debug_configure(1, 20_000_000) == 0  # no copies, 20 ms a wait
         fa().cache_forward(q.cuda(), c, table.cuda(), ints([500]), causal=True)
         code = status()
-        kernel = 12 if cache_ref.many_rows(2, 1, Nq, d) else 11
+        kernel = 12 if cache_ref.many_rows(2, 1, Nq) else 11
         assert code & BAD_INDEX == 0x80000000 and (code >> 16) & 0x3FFF == kernel
     finally:
         lib.fa_debug_configure(0, 0)
