@@ -191,6 +191,19 @@ __device__ __forceinline__ float expand_max(float x, volatile float *red, int dw
   return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
 
+// Bits of the 16 slots of a cell whose token is one of the first `tokens`; none
+// unless bit 0 of `found` is set. (Slots 0, 2, 4, 6 are tokens 0 - 3, slots 1, 3,
+// 5, 7 tokens 4 - 7, and so on: cell_slot.)
+__device__ __forceinline__ uint32_t seen_slots(int tokens, uint32_t found) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int four = min(max(tokens - 4 * x, 0), 4);
+    bits |= ((0x55u >> (8 - 2 * four)) & 0x55u) << ((x & 1) + 8 * (x >> 1));
+  }
+  return (found & 1u) ? bits : 0u;
+}
+
 // The power of two at or below x > 0 times 2^-7, between 2^-120 and 2^120 (1 for 0): what
 // brings values up to x below 2^8.
 __device__ __forceinline__ int tile_exponent(float x) {
@@ -622,10 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = tok < n;
       const bool warp_live = p.by_group.div(tile_row0 + (warp & 3) * 32) < n;  // its first row's token
       const bool has_rows = kTurns || t == 0 || (kNT == 2 && tile_row0 < p.nq * p.group);
-      // The row scaled by a power of two, its largest element below 2^11. A thread
-      // copies its own row to where the product reads it and scales it there: all
-      // of it is on its way at once, in little code (code that runs once a piece
-      // costs most in fetching it).
+      // The row scaled by a power of two, its largest element below 2^11. The rows
+      // are copied to where the product reads them and scaled there, each by its own
+      // thread: all of it is on its way at once, in little code (code that runs once
+      // a piece costs most in fetching it).
       float c_row = 0.f;
       float *const row_scale = reinterpret_cast<float *>(smem + L::kRowScale);
       if (kNT == 2 || t == 0) {
@@ -635,9 +648,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto at = [&](int x) {
           return own + (x >> 3) * (kRows * 128) + (((x & 7) ^ (r & 7)) << 4);
         };
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) cp_async16(at(x), src + x * 8, live ? 16 : 0);
+        // eight lanes copy 128 bytes of a row, four rows at a time
+        const uint32_t rows32 = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQBytes + (warp & 3) * 4096;
+#pragma unroll 2
+        for (int y = 0; y < 8; ++y) {
+          const int rr = 4 * y + (lane >> 3);
+          const uint16_t *const row_src = reinterpret_cast<const uint16_t *>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), rr));
+          const bool row_live = __shfl_sync(0xffffffffu, (int)live, rr);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            if (c * 8 + (lane & 7) < D / 8)
+              cp_async16(rows32 + c * (kRows * 128) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4),
+                         row_src + c * 64 + (lane & 7) * 8, row_live ? 16 : 0);
+        }
         cp_async_wait_all();
+        __syncwarp();
         uint32_t top2 = 0;  // the largest magnitudes of the even and the odd channels
 #pragma unroll 4
         for (int x = 0; x < D / 8; ++x) {
@@ -702,33 +728,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = piece.t0 * kUnitTokens + k * kKeys;
         const bool masked = key0 + kKeys > all || found != (1u << kTileCells) - 1;
         const int left = min(lim, vis) - key0;
-        // scores of keys 64 half .. 64 half + 63 (slots), hidden ones -inf
-        auto load_scores = [&](int half, float (&x64)[64]) {
-          uint32_t sr[2][32];
-          tmem_ld32(tS + half * 64, sr[0]);
-          tmem_ld32(tS + half * 64 + 32, sr[1]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 64; ++x) x64[x] = __uint_as_float(sr[x >> 5][x & 31]);
-          if (masked) {
-            const int from = left - half * 64;
-            const uint32_t cells4 = found >> (half * 4);
-#pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if ((x & ~15) + cell_token(x & 15) >= from || !((cells4 >> (x >> 4)) & 1))
-                x64[x] = -INFINITY;
-          }
-        };
         float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int half = 0; half < kKeys / 64; ++half) {
-          float x64[64];
-          load_scores(half, x64);
+        for (int q = 0; q < kKeys / 32; ++q) {
+          uint32_t x32[32];
+          tmem_ld32(tS + q * 32, x32);
+          tmem_wait_ld();
+          if (masked) {  // hidden scores become -inf, for the second reading too
+            const uint32_t seen = seen_slots(left - q * 32, found >> (2 * q)) |
+                                  seen_slots(left - q * 32 - 16, found >> (2 * q + 1)) << 16;
 #pragma unroll
-          for (int x = 0; x < 64; x += 8)
+            for (int x = 0; x < 32; ++x)
+              if (!(seen & (1u << x))) x32[x] = 0xff800000u;
+            tmem_st32(tS + q * 32, x32);
+          }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mp[y] = fmax3(mp[y], x64[x + 2 * y], x64[x + 2 * y + 1]);
+          for (int x = 0; x < 32; x += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              mp[y] = fmax3(mp[y], __uint_as_float(x32[x + 2 * y]),
+                            __uint_as_float(x32[x + 2 * y + 1]));
         }
+        if (masked) tmem_wait_st();
         ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.v_scale(i & 1), (i >> 1) & 1, st,
                                                    code(kRoleSoftmax, 5)));
         if (!ok) break;
@@ -749,20 +770,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ct2 = f2pack(ct, ct), sub2 = f2pack(sub, sub);
         uint64_t sum[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll 1
-        for (int half = 0; half < kKeys / 64; ++half) {
-          float x64[64];
-          load_scores(half, x64);
-          uint32_t pk[32];
+        for (int q = 0; q < kKeys / 32; ++q) {
+          uint32_t x32[32];
+          tmem_ld32(tS + q * 32, x32);
+          tmem_wait_ld();
+          uint32_t pk[16];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < 16; ++x) {
             float a, b;
-            f2unpack(ffma2(f2pack(x64[2 * x], x64[2 * x + 1]), ct2, sub2), a, b);
+            f2unpack(ffma2(f2pack(__uint_as_float(x32[2 * x]), __uint_as_float(x32[2 * x + 1])), ct2,
+                           sub2),
+                     a, b);
             a = ex2_approx(a);
             b = ex2_approx(b);
             sum[x & 1] = fadd2(sum[x & 1], f2pack(a, b));
             pk[x] = pack_f16x2(a, b);
           }
-          tmem_st32(tS + 32 * half, pk);
+          tmem_st16(tS + 16 * q, pk);
         }
         float la, lb;
         f2unpack(fadd2(sum[0], sum[1]), la, lb);
@@ -861,7 +885,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t prow = ((size_t)blockIdx.x * 2 + (pieces ? 1 : 0)) * kBlockRows + (row - piece.row0);
         const bool store = tok < p.nq;  // (nothing reads the other rows)
         const size_t at = store && whole ? p.so.row(piece.b, hq, tok) : 0;
-        float *const to32 = whole ? static_cast<float *>(p.o) + at : p.part + prow * D;
+        // a lane's row goes through shared memory (Q's, which nothing reads now), 32
+        // columns at a time, so that eight lanes store 128 bytes of a row: 32 rows
+        // a store would take 32 cycles
+        const bool wide = !whole || p.o_f32;
+        uint8_t *const to =
+            !store   ? nullptr
+            : !whole ? reinterpret_cast<uint8_t *>(p.part + prow * D)
+                     : static_cast<uint8_t *>(p.o) + at * (p.o_f32 ? 4 : 2);
+        const uint32_t mine32 = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQBytes + (warp & 3) * 4096;
 #pragma unroll 1
         for (int q = 0; q < kG; ++q) {
           uint32_t o[32];
@@ -869,27 +901,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + q * 32, o);
             tmem_wait_ld();
           }
-          const bool spoiled = (nan_groups >> q) & 1;
-          float v[32];
+          // (a NaN among V's group spoils all of its channels)
+          const float by = (nan_groups >> q) & 1 ? __uint_as_float(0x7fffffffu) : inv;
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            v[x] = none      ? 0.f
-                   : spoiled ? __uint_as_float(0x7fffffffu)
-                             : __uint_as_float(o[x]) * inv;
-          if (!store) {
-          } else if (!whole || p.o_f32) {
-            float4 *const dst = reinterpret_cast<float4 *>(to32 + q * 32);
+            o[x] = none ? 0u : __float_as_uint(__uint_as_float(o[x]) * by);
+          __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              dst[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-          } else {
-            uint4 *const dst =
-                reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + at + q * 32);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              dst[x] = make_uint4(
-                  pack2<kF16>(v[8 * x], v[8 * x + 1]), pack2<kF16>(v[8 * x + 2], v[8 * x + 3]),
-                  pack2<kF16>(v[8 * x + 4], v[8 * x + 5]), pack2<kF16>(v[8 * x + 6], v[8 * x + 7]));
+          for (int x = 0; x < 8; ++x)
+            sts128(mine32 + lane * 128 + ((x ^ (lane & 7)) << 4), o[4 * x], o[4 * x + 1],
+                   o[4 * x + 2], o[4 * x + 3]);
+          __syncwarp();
+          const int piece4 = lane & 7;  // columns 4 piece4 .. of the 32
+#pragma unroll 2
+          for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + (lane >> 3);
+            uint8_t *const row_to = reinterpret_cast<uint8_t *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), rr));
+            uint32_t w[4];
+            lds128(mine32 + rr * 128 + ((piece4 ^ (rr & 7)) << 4), w[0], w[1], w[2], w[3]);
+            if (!row_to) {
+            } else if (wide) {
+              reinterpret_cast<uint4 *>(row_to)[q * 8 + piece4] = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              reinterpret_cast<uint2 *>(row_to)[q * 8 + piece4] =
+                  make_uint2(pack2<kF16>(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                             pack2<kF16>(__uint_as_float(w[2]), __uint_as_float(w[3])));
+            }
           }
         }
         if (store) {
