@@ -830,42 +830,78 @@ __global__ void __launch_bounds__(kCombineThreads)
   }
   const int last = s_last;
   const int sub = threadIdx.x / kChunks, chunk = threadIdx.x - sub * kChunks;
-  for (int row = blockIdx.y; row < kRows; row += gridDim.y) {
-    const int tok = p.by_group.div(row0 + row), hq = c.y * p.group + (row0 + row - tok * p.group);
-    if (tok >= p.nq) return;  // (nor are the rows behind it tokens)
-    if (sub < kSub) {
-      float top = -INFINITY, sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kBatch = 4;
-      for (int s0 = x + sub; s0 <= last; s0 += kBatch * kSub) {
-        float lse2[kBatch];
-        float4 a[kBatch];
+
+  // every `step`-th part from `from` on: their largest LSE, and sums scaled by it
+  float top, sum;
+  float4 o;
+  auto add_parts = [&](int row, int from, int step) {
+    top = -INFINITY;
+    sum = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;
+    for (int s0 = from; s0 <= last; s0 += kBatch * step) {
+      float lse2[kBatch];
+      float4 a[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int s = s0 + i * kSub;
-          const size_t prow = ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
-          lse2[i] = s <= last ? p.part_lse[prow] : -INFINITY;
-          a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (s <= last) a[i] = *reinterpret_cast<const float4 *>(p.part + prow * D + chunk * 4);
-        }
-        float high = top;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) high = fmaxf(high, lse2[i]);
-        if (top != -INFINITY) {
-          const float corr = ex2_approx(top - high);
-          sum *= corr;
-          o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
-        }
-        top = high;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          // (a part without keys counts nothing; a NaN goes on)
-          const float w = lse2[i] == -INFINITY ? 0.f : ex2_approx(lse2[i] - top);
-          sum += w;
-          o = make_float4(fmaf(w, a[i].x, o.x), fmaf(w, a[i].y, o.y), fmaf(w, a[i].z, o.z),
-                          fmaf(w, a[i].w, o.w));
-        }
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + i * step;
+        const size_t prow = ((size_t)s * 2 + (s == x ? c.z : 0)) * kRows + row;
+        lse2[i] = s <= last ? p.part_lse[prow] : -INFINITY;
+        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s <= last) a[i] = *reinterpret_cast<const float4 *>(p.part + prow * D + chunk * 4);
       }
+      float high = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) high = fmaxf(high, lse2[i]);
+      if (top != -INFINITY) {
+        const float corr = ex2_approx(top - high);
+        sum *= corr;
+        o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
+      }
+      top = high;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // (a part without keys counts nothing; a NaN goes on)
+        const float w = lse2[i] == -INFINITY ? 0.f : ex2_approx(lse2[i] - top);
+        sum += w;
+        o = make_float4(fmaf(w, a[i].x, o.x), fmaf(w, a[i].y, o.y), fmaf(w, a[i].z, o.z),
+                        fmaf(w, a[i].w, o.w));
+      }
+    }
+  };
+  auto store = [&](int row, int tok) {  // 4 columns of the row, by the threads of its chunks
+    const int hq = c.y * p.group + (row0 + row - tok * p.group);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t at = p.so.row(b, hq, tok) + chunk * 4;
+    if (p.o_f32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
+          make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
+    if (chunk == 0)
+      p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
+          sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
+  };
+
+  // Few parts: the threads of a column merge them by themselves, and the kSub
+  // sets of threads take rows of their own (a chunk of 1024 tokens, two or three
+  // parts each).
+  if (last - x < (kRows >= 128 ? 8 : 4)) {
+    if (sub >= kSub) return;
+    for (int row = blockIdx.y + sub * gridDim.y; row < kRows; row += kSub * gridDim.y) {
+      const int tok = p.by_group.div(row0 + row);
+      if (tok >= p.nq) return;  // (nor are the rows behind it tokens)
+      add_parts(row, x, 1);
+      store(row, tok);
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < kRows; row += gridDim.y) {
+    const int tok = p.by_group.div(row0 + row);
+    if (tok >= p.nq) return;
+    if (sub < kSub) {
+      add_parts(row, x + sub, kSub);
       s_o[sub][chunk] = o;
       if (chunk == 0) {
         s_top[sub] = top;
@@ -873,9 +909,10 @@ __global__ void __launch_bounds__(kCombineThreads)
       }
     }
     __syncthreads();
-    if (threadIdx.x < kChunks) {
-      float top = -INFINITY, sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sub == 0) {
+      top = -INFINITY;
+      sum = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kSub; ++i) top = fmaxf(top, s_top[i]);
 #pragma unroll
@@ -883,22 +920,12 @@ __global__ void __launch_bounds__(kCombineThreads)
         if (s_sum[i] == 0.f) continue;
         // a NaN among a thread's parts leaves its top finite or at -inf and its sum NaN
         const float w = s_top[i] == -INFINITY ? 1.f : ex2_approx(s_top[i] - top);
-        const float4 a = s_o[i][threadIdx.x];
+        const float4 a = s_o[i][chunk];
         sum = fmaf(w, s_sum[i], sum);
         o = make_float4(fmaf(w, a.x, o.x), fmaf(w, a.y, o.y), fmaf(w, a.z, o.z),
                         fmaf(w, a.w, o.w));
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t at = p.so.row(b, hq, tok) + threadIdx.x * 4;
-      if (p.o_f32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
-            make_uint2(pack2<kF16>(o.x * inv, o.y * inv), pack2<kF16>(o.z * inv, o.w * inv));
-      if (threadIdx.x == 0)
-        p.lse[((size_t)b * p.hq + hq) * p.nq + tok] =
-            sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
+      store(row, tok);
     }
     __syncthreads();
   }
