@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     top = -INFINITY;
     sum = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
+    constexpr int kBatch = D == 256 ? 8 : 4;  // (d = 256: 4 sequences of 76 parts 12.4 -> 10.3 us)
     for (int s0 = from; s0 <= last; s0 += kBatch * step) {
       float lse2[kBatch];
       float4 a[kBatch];
@@ -937,7 +937,8 @@ cudaError_t launch_combine(const CacheFwdParams &p, cudaStream_t stream) {
   LaunchProbe probe(kKindCacheCombine, stream);
   const long long rows = (long long)p.nq * p.group;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas, (unsigned)(rows < kCombineRows ? rows : kCombineRows));
+  const long long used = rows < kRows ? rows : kRows;
+  cfg.gridDim = dim3(p.ctas, (unsigned)(used < kCombineRows ? used : kCombineRows));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
