@@ -600,12 +600,14 @@ fa_status cache_rows_impl(const fa_cache *cache, const fa_tensor *K, const fa_te
 // Scratch of the attention over a cache: two partial results (fp32 O rows and
 // log2-sum-exp) and one chain record per CTA of a full GPU.
 struct CacheScratch {
-  int ctas;
+  int ctas, block_rows;
   size_t part, lse, chain;
 };
-bool cache_scratch(int sms, int Hq, int Hk, int Nq, int d, long long tokens, CacheScratch *out) {
+bool cache_scratch(int sms, int B, int Hq, int Hk, int Nq, int d, long long tokens,
+                   CacheScratch *out) {
   if (sms <= 0 || Hk <= 0) return false;
-  const int block_rows = fa::cache_forward_block_rows(d, (long long)(Hq / Hk) * Nq);
+  const int block_rows = out->block_rows = fa::cache_forward_block_rows(
+      d, (long long)(Hq / Hk) * Nq, fa::cache_forward_whole(tokens), (double)B * Hk, sms);
   out->ctas = sms * fa::cache_forward_ctas_per_sm(d, block_rows);
   const size_t rows = (size_t)out->ctas * 2 * block_rows;
   out->part = round_up(rows * d * sizeof(float));
@@ -648,7 +650,7 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
     return FA_ERR_MISALIGNED;
   if ((s = bind_device(cache->data)) != FA_OK) return s;
   CacheScratch w;
-  if (!cache_scratch(sm_count(), Hq, cache->heads, Nq, d, tokens, &w))
+  if (!cache_scratch(sm_count(), B, Hq, cache->heads, Nq, d, tokens, &w))
     return cuda_fail("SM count", cudaErrorInvalidDevice);
   if (ws_bytes < w.part + w.lse + w.chain) {
     snprintf(g_last_error, sizeof(g_last_error), "workspace of %zu bytes, %zu needed", ws_bytes,
@@ -672,6 +674,7 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
   p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.part);
   p.chain = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + w.part + w.lse);
   p.ctas = w.ctas;
+  p.block_rows = w.block_rows;
   p.debug_flags = g_debug_flags.load();
   p.wait_limit_ns = g_wait_limit_ns.load() ? g_wait_limit_ns.load() : fa::kWaitLimitNs;
   cudaError_t e = status_word(&p.status);
@@ -968,7 +971,7 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
 size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d, int max_tokens) {
   if (Hq < 0 || Hk <= 0 || Nq < 0 || max_tokens < 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
   CacheScratch w;
-  return cache_scratch(sm_count(), Hq, Hk, Nq, d, max_tokens, &w) ? w.part + w.lse + w.chain : 0;
+  return cache_scratch(sm_count(), 1, Hq, Hk, Nq, d, max_tokens, &w) ? w.part + w.lse + w.chain : 0;
 }
 
 fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,

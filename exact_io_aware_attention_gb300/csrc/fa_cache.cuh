@@ -159,6 +159,7 @@ struct CacheFwdParams {
   float *part;                        // scratch: [ctas][2][rows][d] partial outputs,
   float *part_lse;                    // [ctas][2][rows] their log2-sum-exp,
   int4 *chain;                        // [ctas] where a segment's parts lie
+  int block_rows;                     // query rows of a CTA
   int whole;                          // no segment is split: no scratch, no merge
   int ctas;                           // CTAs of the attention kernel
   unsigned int *status;
@@ -170,22 +171,10 @@ cudaError_t launch_cache_write(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsParams &p, cudaStream_t stream);
 cudaError_t launch_cache_forward(const CacheFwdParams &p, cudaStream_t stream);
 
-// The attention with 128 or 256 query rows a CTA on tcgen05 (fa_cache_fwd_tc.cu),
-// d up to 128; the merge of its parts is launched by launch_cache_forward.
-cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows, cudaStream_t stream);
+// The attention with 128 or 256 query rows a CTA on tcgen05 (fa_cache_fwd_tc.cu);
+// the merge of its parts is launched by launch_cache_forward.
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream);
 
-// Query rows (new tokens times query heads of one K/V head) that one CTA
-// holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
-// tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
-// in the one for many. Measured, 16 sequences of 6600 keys, 2 K/V heads, d = 128
-// (few / many): 24 rows 36 / 58 us, 64 rows 57 / 63 us, 96 rows 68 / 69 us (bf16)
-// and 78 / 69 us (f16), 128 rows 98 / 74 us; 4 sequences of 4000 keys, 12 heads,
-// d = 64: 64 rows 40 / 49 us, 100 rows 57 / 53 us.
-constexpr int cache_forward_block_rows(int d, long long rows) {
-  return d == 256   ? (rows <= 64 ? 8 : 128)
-         : rows <= 8 ? 8
-                     : rows <= 64 ? 16 : rows <= 128 ? 128 : 256;
-}
 // CTAs that one SM holds (its registers and shared memory allow).
 constexpr int cache_forward_ctas_per_sm(int d, int block_rows) {
   return block_rows >= 128 ? 1
@@ -195,4 +184,29 @@ constexpr int cache_forward_ctas_per_sm(int d, int block_rows) {
 
 // Whether sequences of at most `tokens` tokens are not split between CTAs.
 constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
+
+// Query rows (new tokens times query heads of one K/V head) that one CTA
+// holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
+// tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
+// (d = 256: 128) in the one for many.
+//
+// Where the work is split over the keys, by the rows that share an expansion.
+// Measured, 16 sequences of 5000 to 8192 keys, 2 K/V heads (few / many, whole
+// calls): 32 rows, bf16, 34 / 38 us at d = 64, 39 / 48 us at d = 128, 58 / 79 us at
+// d = 256; 40 rows, f16, 39 / 38, 52 / 48 and 81 / 79 us; 64 rows, bf16, 44 / 38,
+// 54 / 48 and 97 / 81 us.
+//
+// Where a segment stays whole, the few-row kernel is done sooner as long as all
+// its segments run at once (d = 256: in two turns), and 128 rows sooner than 256
+// as long as they do. Measured, up to 1000 keys, d = 128 (few / many): 8 heads
+// of 512 rows, 256 segments, 23 / 36 us; 64 heads of 128 rows, 512 segments,
+// 38 / 28 us; 12 heads of 1000 rows NNN.
+constexpr int cache_forward_block_rows(int d, long long rows, bool whole, double heads, int sms) {
+  const int few = d == 256 || rows <= 8 ? 8 : 16;
+  if (rows <= 32) return few;
+  if (whole && heads * ((rows + few - 1) / few) <=
+                   (d == 256 ? 2.0 : 1.0) * sms * cache_forward_ctas_per_sm(d, few))
+    return few;
+  return d == 256 || rows <= 128 || (whole && heads * ((rows + 127) / 128) <= sms) ? 128 : 256;
+}
 }  // namespace fa

@@ -963,7 +963,7 @@ cudaError_t launch_d(const CacheFwdParams &p, cudaStream_t stream) {
 template <int D, bool kF16>
 cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
   CacheFwdParams p = all;
-  const int rows = cache_forward_block_rows(D, (long long)p.nq * p.group);
+  const int rows = p.block_rows;
   const int row_blocks = (p.nq * p.group + rows - 1) / rows;
   p.by_row_blocks = FastDiv(row_blocks);
   // no more CTAs than shares of sequences as long as the table could have
@@ -975,7 +975,7 @@ cudaError_t launch_t(const CacheFwdParams &all, cudaStream_t stream) {
   if (shares < (double)p.ctas) p.ctas = (int)shares + 1;
   cudaError_t e;
   if (rows >= 128)
-    e = launch_cache_forward_tc(p, rows, stream);
+    e = launch_cache_forward_tc(p, stream);
   else if constexpr (D == 256)
     e = launch_d<D, 1, kF16>(p, stream);
   else

@@ -266,20 +266,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int heads = p.pool.heads;
 
   // Every role walks over the same pieces, tiles [piece.t0, piece.t0 + count) of
-  // a segment; tile0 counts the tiles before a piece (buffers and parities).
-  // work(piece, count, tile0, pieces) ends with the barrier of all threads.
+  // a segment; tile0 counts the tiles before a piece (buffers and parities), tile1
+  // those of them in which the second 128 rows took part.
+  // work(piece, count, tile0, tile1, pieces) ends with the barrier of all threads.
   int4 chain = make_int4(-1, 0, 0, 0);
   bool failed = false;
+  auto has_second = [&](const Piece &piece) {
+    return kNT == 2 && piece.row0 + kRows < p.nq * p.group;
+  };
   auto walk = [&](auto work) {
     long long f = mine.f;
-    uint32_t tile0 = 0, pieces = 0;
+    uint32_t tile0 = 0, tile1 = 0, pieces = 0;
     while (mine.found && f < mine.f_end) {
       const Piece piece(p, blocks, misc, f, mine.f_end);
       if (piece.h < 0 || piece.h >= heads) break;
       constexpr int kPerUnit = kUnitTokens / kKeys;
       const int count = max(0, min(piece.t1 * kPerUnit, (piece.cells + kTileCells - 1) / kTileCells) -
                                    piece.t0 * kPerUnit);
-      work(piece, count, tile0, pieces);
+      work(piece, count, tile0, tile1, pieces);
       tc_fence_before();
       __syncthreads();
       tc_fence_after();
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (failed) break;
       piece.link(chain, pieces == 0);
       tile0 += count;
+      if (has_second(piece)) tile1 += count;
       ++pieces;
       f = piece.next(p);
       if (!piece.advance(p, blocks, misc, f)) break;
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsIssue>();
-    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t pieces) {
+    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t tile1, uint32_t pieces) {
       const int cells = piece.cells, cell0 = piece.t0 * (kUnitTokens / kCellTokens);
     if (warp == 0) {
       // ---- copies ----------------------------------------------------------
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one() && count > 0) {
         constexpr uint32_t kIdS = idesc_f32acc(kRows, kKeys, 0, 0, true);
         constexpr uint32_t kIdPV = idesc_f32acc(kRows, D, 0, 0, true);
-        const bool two = kNT == 2 && piece.row0 + kRows < p.nq * p.group;  // t = 1 has rows
+        const bool two = has_second(piece);
         // (a descriptor's low bits are the address in units of 16 bytes)
         const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);
         const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = k + 1 < count;
             ok = mbar_wait_inl(bars.v_full(i & 1), (i >> 1) & 1, st, code(kRoleMma, 3));
             for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
-              ok = mbar_wait_inl(bars.p_full(t), i & 1, st, code(kRoleMma, 4 + t));
+              ok = mbar_wait_inl(bars.p_full(t), (t ? tile1 + k : i) & 1, st, code(kRoleMma, 4 + t));
               if (!ok) break;
               tc_fence_after();
               issue_pv(t, i, k == 0);
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dt = threadIdx.x & 127, dw = warp & 3;
     if (warp < 16) {
       // ---- expansion of K ---------------------------------------------------
-      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t) {
+      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t, uint32_t) {
         bool ok = true;
         for (int k = 0; k < count; ++k) {
           const uint32_t i = tile0 + k;
@@ -529,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       });
     } else {
       // ---- expansion of V ---------------------------------------------------
-      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t) {
+      walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t, uint32_t) {
         bool ok = true;
         for (int k = 0; k < count; ++k) {
           const uint32_t i = tile0 + k;
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
-    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t pieces) {
+    walk([&](const Piece &piece, int count, uint32_t tile0, uint32_t tile1, uint32_t pieces) {
       const int n = piece.n, len = piece.len, vis = piece.vis;
       // keys before `all` are visible to every row that is a token
       const int all = p.causal ? min(vis, len - n + p.by_group.div(piece.row0) + 1) : vis;
@@ -634,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = p.by_group.div(row), hq = piece.h * p.group + (row - tok * p.group);
       const bool live = tok < n;
       const bool warp_live = p.by_group.div(tile_row0 + (warp & 3) * 32) < n;  // its first row's token
-      const bool has_rows = kTurns || t == 0 || (kNT == 2 && tile_row0 < p.nq * p.group);
+      const bool has_rows = kTurns || t == 0 || has_second(piece);
+      const uint32_t own0 = t == 0 ? tile0 : tile1;  // this warpgroup's tiles before (no turns)
       // The row scaled by a power of two, its largest element below 2^11. The rows
       // are copied to where the product reads them and scaled there, each by its own
       // thread: all of it is on its way at once, in little code (code that runs once
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;
       for (int k = kTurns ? ((tile0 ^ t) & 1) : 0; k < count && has_rows && ok; k += kTurns ? 2 : 1) {
         const uint32_t i = tile0 + k;
-        const uint32_t parity = (kTurns ? i >> 1 : i) & 1;
+        const uint32_t parity = (kTurns ? i >> 1 : own0 + k) & 1;
         ok = __all_sync(0xffffffffu,
                         mbar_wait_inl(bars.s_full(t), parity, st, code(kRoleSoftmax, 1)));
         if (!ok) break;
@@ -813,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- O / l and the log-sum-exp -------------------------------------------
       if constexpr (!kTurns) {
         if (ok && any)
-          ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(t), (tile0 + count - 1) & 1, st,
+          ok = __all_sync(0xffffffffu, mbar_wait_inl(bars.pv_done(t), (own0 + count - 1) & 1, st,
                                                      code(kRoleSoftmax, 2)));
         tc_fence_after();
       } else {
@@ -970,9 +976,8 @@ cudaError_t launch_tc_rows(const CacheFwdParams &p, bool two, cudaStream_t strea
 
 }  // namespace
 
-cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, int block_rows,
-                                    cudaStream_t stream) {
-  const bool f16 = p.pool.f16 != 0, two = block_rows == 256;
+cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream) {
+  const bool f16 = p.pool.f16 != 0, two = p.block_rows == 256;
   switch (p.pool.d) {
     case 64: return f16 ? launch_tc_rows<64, true>(p, two, stream) : launch_tc_rows<64, false>(p, two, stream);
     case 96: return f16 ? launch_tc_rows<96, true>(p, two, stream) : launch_tc_rows<96, false>(p, two, stream);

@@ -13,7 +13,8 @@ comes with bounds on the rounding errors of the library's kernels:
     approximate exponential adds 2^-21;
   * the result is rounded to the output's type: half a step, eps / 2.
 
-With more than 64 query rows a K/V head K, V and P are f16
+With more than 32 query rows a K/V head there is another kernel, for some of the
+sizes, and the bound is the larger one. In it K, V and P are f16
 operands of the tensor cores: half a step is 2^-11 of each value (of K and V,
 scaled by a power of two to below 2^8 a tile of keys, 2^-25 below f16's normal
 range, so 2^-32 of the tile's largest; of P, whose largest is at least 1, 2^-25).
@@ -55,10 +56,6 @@ def read_back(x):
     return torch.from_numpy(y.astype(np.float32).reshape(x.shape)).to(x.dtype)
 
 
-def many_rows(Hq, Hk, Nq):
-    return Hq // Hk * Nq > 64
-
-
 def attend(q, k, v, n, causal, scale, out_eps):
     """Attention of one sequence and the error bounds of its outputs.
 
@@ -68,7 +65,7 @@ def attend(q, k, v, n, causal, scale, out_eps):
     """
     Hq, Nq, d = q.shape
     Hk, L, _ = k.shape
-    f16_operands = many_rows(Hq, Hk, Nq)
+    f16_operands = Hq // Hk * Nq > 32  # possibly
     O, lse = np.zeros((Hq, Nq, d)), np.full((Hq, Nq), -np.inf)
     tO, tl = np.zeros((Hq, Nq, d)), np.zeros((Hq, Nq))
     for h in range(Hk):
@@ -92,17 +89,18 @@ def attend(q, k, v, n, causal, scale, out_eps):
                 O[hq, i] = p @ vd[:m]
                 lse[hq, i] = top + np.log(l)
                 rel = 2 * e.max() + 2.0 ** -20 + m * 2.0 ** -24  # of p / l
+                w = (p[:, None] * vstep[:m])
+                tO[hq, i] = (2.0 ** -11 * w.sum(0) + m * 2.0 ** -25 * w.max() +
+                             2 * rel * (p @ (np.abs(vd[:m]) + 2 * vstep[:m])))
                 if f16_operands:
                     av, ak = np.abs(vd[:m]), np.abs(kd[:m])
                     ek = scale * ((2.0 ** -11 * ak + 2.0 ** -32 * ak.max()) @ np.abs(qd[i])).max()
                     rel += 2 * ek
                     tl[hq, i] = ek
-                    tO[hq, i] = (2 * 2.0 ** -11 * (p @ av) + m * 2.0 ** -24 * p.max() * av.max() +
-                                 2.0 ** -32 * av.max() + 2 * rel * (p @ av))
-                else:
-                    w = (p[:, None] * vstep[:m])
-                    tO[hq, i] = (2.0 ** -11 * w.sum(0) + m * 2.0 ** -25 * w.max() +
-                                 2 * rel * (p @ (np.abs(vd[:m]) + 2 * vstep[:m])))
+                    tO[hq, i] = np.maximum(
+                        tO[hq, i],
+                        2 * 2.0 ** -11 * (p @ av) + m * 2.0 ** -24 * p.max() * av.max() +
+                        2.0 ** -32 * av.max() + 2 * rel * (p @ av))
                 tO[hq, i] += out_eps / 2 * (np.abs(O[hq, i]) + tO[hq, i])
                 tl[hq, i] += e.max() + 2.0 ** -20 + m * 2.0 ** -24 + 2.0 ** -22 * abs(lse[hq, i])
     return O, lse, tO, tl

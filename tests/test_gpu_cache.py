@@ -36,6 +36,13 @@ def random_table(B, pages, seed, spare=3):
     return torch.randperm(n, generator=g)[:B * pages].reshape(B, pages).to(torch.int32), n
 
 
+def widen(table, page):
+    """The table with room for more than 1024 tokens, beyond which sequences are split between
+    CTAs and 33 rows a K/V head count as many. What the new entries say is never read."""
+    return torch.cat([table, torch.full((table.shape[0], 1024 // page + 1), 1 << 30,
+                                        dtype=torch.int32, device=table.device)], 1)
+
+
 def new_cache(n_pages, H, d, page, dtype, fill=0xFF):
     """A cache whose untouched groups read as NaN."""
     c = fa().KVCache4(n_pages, H, d, page_size=page, dtype=dtype)
@@ -177,13 +184,15 @@ def compare(o, lse, q, k, v, lengths, counts, causal, scale, what):
 
 
 def attend_case(B, Hq, Hk, Nq, lengths, d, page, dtype, causal, counts=None, scale=None, o32=True,
-                v_scale=1.0, k_scale=1.0, what=""):
+                v_scale=1.0, k_scale=1.0, wide=False, what=""):
     L = max(lengths)
     k = (rand((B, Hk, max(L, 1), d), 31, dtype).float() * k_scale +
          rand((1, Hk, 1, d), 32, dtype).float() * k_scale).to(dtype)
     v = (rand((B, Hk, max(L, 1), d), 33, dtype).float() * v_scale).to(dtype)
     q = rand((B, Hq, Nq, d), 34, dtype)
     table, pool = random_table(B, max(1, -(-L // page)), seed=Nq + d)
+    if wide:
+        table = widen(table, page)
     c = new_cache(pool, Hk, d, page, dtype)
     fa().cache_write(c, k.cuda(), v.cuda(), table.cuda(), ints([0] * B), ints(lengths))
     cnt = None if counts is None else ints(counts)
@@ -225,7 +234,8 @@ def test_rows_that_see_nothing(d, dtype):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("Nq,Hq,Hk", [(130, 2, 1), (33, 4, 2), (257, 1, 1)])
 def test_chunks_of_a_prompt(d, Nq, Hq, Hk):
-    attend_case(2, Hq, Hk, Nq, [Nq, Nq + 500], d, 64, BF16, True, o32=False, what="chunk")
+    attend_case(2, Hq, Hk, Nq, [Nq, Nq + 500], d, 64, BF16, True, o32=False, wide=True,
+                what="chunk")
     attend_case(2, Hq, Hk, Nq, [Nq + 77, Nq], d, 32, F16, True, counts=[Nq - 5, Nq], what="chunk f16")
 
 
@@ -242,9 +252,36 @@ def test_chunks_of_a_prompt(d, Nq, Hq, Hk):
     (5, 3, 1, 100, [1300, 128, 127, 700, 100], 32, None),  # pieces that begin at odd tiles
 ])
 def test_many_rows(d, dtype, B, Hq, Hk, Nq, lengths, page, counts):
-    for causal in (True, False):
-        attend_case(B, Hq, Hk, Nq, lengths, d, page, dtype, causal, counts=counts,
-                    what=f"{d} {dtype} {causal} {lengths}")
+    for causal, wide in ((True, True), (False, True), (True, False)):
+        attend_case(B, Hq, Hk, Nq, lengths, d, page, dtype, causal, counts=counts, wide=wide,
+                    what=f"{d} {dtype} {causal} {wide} {lengths}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_row_blocks_of_different_heights(d):
+    """260 rows a K/V head are 256 and 4: CTAs walk over both kinds, at odd and even tiles."""
+    B, Hk, Nq = 24, 8, 130
+    lengths = [130 + (i * 97) % 400 for i in range(B)]
+    table, pool = random_table(B, max(lengths) // 32 + 1, seed=7)
+    table = widen(table, 32)
+    k, v = rand((B, Hk, max(lengths), d), 151, BF16), rand((B, Hk, max(lengths), d), 152, BF16)
+    q = rand((B, 2 * Hk, Nq, d), 153, BF16)
+    c = new_cache(pool, Hk, d, 32, BF16)
+    fa().cache_write(c, k.cuda(), v.cuda(), table.cuda(), ints([0] * B), ints(lengths))
+    o, lse = fa().cache_forward(q.cuda(), c, table.cuda(), ints(lengths), causal=True)
+    clean()
+    for b in (0, 11, 23):
+        compare(o[b:b + 1, :4], lse[b:b + 1, :4], q[b:b + 1, :4], k[b:b + 1, :2], v[b:b + 1, :2],
+                lengths[b:b + 1], None, True, None, b)
+
+
+@pytest.mark.parametrize("d,dtype,B", [(64, F16, 7), (64, BF16, 10), (96, BF16, 7), (128, F16, 10),
+                                       (128, BF16, 7), (256, BF16, 7)])
+def test_many_rows_of_short_sequences(d, dtype, B):
+    """So many that they do not all run at once with few rows a CTA."""
+    lengths = [(i * 53) % 190 for i in range(B)]
+    attend_case(B, 8, 8, 150, lengths, d, 32, dtype, True, counts=[min(150, n) for n in lengths],
+                o32=False, what="short")
 
 
 @pytest.mark.parametrize("v_scale,k_scale", [(1e-3, 1.0), (300.0, 1.0), (1e-30, 1.0), (1e25, 1.0),
@@ -252,8 +289,10 @@ def test_many_rows(d, dtype, B, Hq, Hk, Nq, lengths, page, counts):
 def test_sizes_of_values(v_scale, k_scale):
     """V far from 1 (the weights p s must keep their bits), sharp and flat scores."""
     attend_case(2, 4, 2, 2, [333, 40], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
-    attend_case(1, 40, 1, 2, [333], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
-    attend_case(1, 40, 1, 2, [333], 256, 32, BF16, True, v_scale=v_scale, k_scale=k_scale)
+    attend_case(1, 40, 1, 2, [333], 128, 32, BF16, True, v_scale=v_scale, k_scale=k_scale,
+                wide=True)
+    attend_case(1, 40, 1, 2, [333], 256, 32, BF16, True, v_scale=v_scale, k_scale=k_scale,
+                wide=True)
     if 1e-4 < v_scale < 1e3 and k_scale > 1e-4:
         attend_case(2, 4, 2, 2, [333, 40], 64, 32, F16, True, v_scale=v_scale, k_scale=k_scale)
 
@@ -327,6 +366,8 @@ def test_non_finite_values_stay_where_they_are_seen(d, Hq):
     k, v, q = (rand(s, 70 + i, BF16) for i, s in
                enumerate(((B, 1, L, d), (B, 1, L, d), (B, Hq, Nq, d))))
     table = ints([[1, 0, 2]])
+    if Hq > 2:
+        table = widen(table, 16)
 
     def run(k, v, q):
         c = new_cache(3, 1, d, 16, BF16)
@@ -612,7 +653,7 @@ def test_bad_pages_with_many_rows(d, page, Hq):
     L, n_pages = 700, -(-700 // page)
     k, v, q = (rand((1, h, n, d), 120 + i, BF16) for i, (h, n) in enumerate(((1, L), (1, L), (Hq, 1))))
     c = new_cache(n_pages, 1, d, page, BF16)
-    good = ints([list(range(n_pages))])
+    good = widen(ints([list(range(n_pages))]), page)
     fa().cache_write(c, k.cuda(), v.cuda(), good, ints([0]))
     assert status() == 0
     bad = good.clone()
@@ -633,7 +674,7 @@ def test_many_rows_from_pages_beyond_32_bit_offsets(d):
     page = 64
     pool = (1 << 32) // (64 * 5 * d // 2) + 3
     c = fa().KVCache4(pool, 1, d, page_size=page)
-    table = ints([[pool - 1, 3, pool - 2]])
+    table = widen(ints([[pool - 1, 3, pool - 2]]), page)
     k, v, q = (rand((1, h, 150, d), 130 + i, BF16) for i, h in enumerate((1, 1, 2)))
     fa().cache_write(c, k.cuda(), v.cuda(), table, ints([0]))
     o, lse = fa().cache_forward(q.cuda(), c, table, ints([150]), causal=True)
@@ -669,12 +710,12 @@ def test_graph_of_many_rows_follows_lengths(Hq, Nq, d):
                                   (256, 20), (256, 40)])
 def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
     lib = binding.load_library()
-    c, table, q, k, v = attend_case(1, 2, 1, Nq, [500], d, 64, BF16, True)
+    c, table, q, k, v = attend_case(1, 2, 1, Nq, [500], d, 64, BF16, True, wide=True)
     try:
         assert lib.fa_debug_configure(1, 20_000_000) == 0  # no copies, 20 ms a wait
         fa().cache_forward(q.cuda(), c, table.cuda(), ints([500]), causal=True)
         code = status()
-        kernel = 12 if cache_ref.many_rows(2, 1, Nq) else 11
+        kernel = 12 if 2 * Nq > 32 else 11
         assert code & BAD_INDEX == 0x80000000 and (code >> 16) & 0x3FFF == kernel
     finally:
         lib.fa_debug_configure(0, 0)
