@@ -190,23 +190,25 @@ constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 // tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
 // (d = 256: 128) in the one for many.
 //
-// Where the work is split over the keys, by the rows that share an expansion.
-// Measured, 16 sequences of 5000 to 8192 keys, 2 K/V heads (few / many, whole
-// calls): 32 rows, bf16, 34 / 38 us at d = 64, 39 / 48 us at d = 128, 58 / 79 us at
-// d = 256; 40 rows, f16, 39 / 38, 52 / 48 and 81 / 79 us; 64 rows, bf16, 44 / 38,
-// 54 / 48 and 97 / 81 us.
+// Up to 64 rows few: the other kernel needs 8 to 15 us more before and after its
+// tiles, which only much work outweighs. Measured (few / many, whole calls), 4
+// sequences of 6000 to 16000 keys on 2 K/V heads, 64 rows, bf16: 31 / 32 us at
+// d = 64, 34 / 40 us at d = 128, 52 / 58 us at d = 256; one of 3000 keys on 4 heads
+// 17 / 21, 18 / 24 and 21 / 32 us; 16 of 5000 to 8192 keys 44 / 38, 54 / 48 and
+// 97 / 81 us. With 128 rows, 4 sequences on 2 heads: 92 / 52 us at d = 256.
 //
 // Where a segment stays whole, the few-row kernel is done sooner as long as all
 // its segments run at once (d = 256: in two turns), and 128 rows sooner than 256
 // as long as they do. Measured, up to 1000 keys, d = 128 (few / many): 8 heads
 // of 512 rows, 256 segments, 23 / 36 us; 64 heads of 128 rows, 512 segments,
-// 38 / 28 us; 12 heads of 1000 rows NNN.
+// 38 / 28 us; 12 heads of 1000 rows (128 / 256 rows a CTA) 27 / 36 us.
 constexpr int cache_forward_block_rows(int d, long long rows, bool whole, double heads, int sms) {
   const int few = d == 256 || rows <= 8 ? 8 : 16;
-  if (rows <= 32) return few;
+  if (rows <= 64) return few;
   if (whole && heads * ((rows + few - 1) / few) <=
                    (d == 256 ? 2.0 : 1.0) * sms * cache_forward_ctas_per_sm(d, few))
     return few;
   return d == 256 || rows <= 128 || (whole && heads * ((rows + 127) / 128) <= sms) ? 128 : 256;
 }
+
 }  // namespace fa

@@ -13,7 +13,7 @@ comes with bounds on the rounding errors of the library's kernels:
     approximate exponential adds 2^-21;
   * the result is rounded to the output's type: half a step, eps / 2.
 
-With more than 32 query rows a K/V head there is another kernel, for some of the
+With more than 64 query rows a K/V head there is another kernel, for some of the
 sizes, and the bound is the larger one. In it K, V and P are f16
 operands of the tensor cores: half a step is 2^-11 of each value (of K and V,
 scaled by a power of two to below 2^8 a tile of keys, 2^-25 below f16's normal
@@ -65,7 +65,7 @@ def attend(q, k, v, n, causal, scale, out_eps):
     """
     Hq, Nq, d = q.shape
     Hk, L, _ = k.shape
-    f16_operands = Hq // Hk * Nq > 32  # possibly
+    f16_operands = Hq // Hk * Nq > 64  # possibly
     O, lse = np.zeros((Hq, Nq, d)), np.full((Hq, Nq), -np.inf)
     tO, tl = np.zeros((Hq, Nq, d)), np.zeros((Hq, Nq))
     for h in range(Hk):

@@ -38,7 +38,7 @@ def random_table(B, pages, seed, spare=3):
 
 def widen(table, page):
     """The table with room for more than 1024 tokens, beyond which sequences are split between
-    CTAs and 33 rows a K/V head count as many. What the new entries say is never read."""
+    CTAs and 65 rows a K/V head count as many. What the new entries say is never read."""
     return torch.cat([table, torch.full((table.shape[0], 1024 // page + 1), 1 << 30,
                                         dtype=torch.int32, device=table.device)], 1)
 
@@ -646,7 +646,7 @@ def test_bad_indices_are_skipped_and_reported():
     assert lib.fa_status_string(6) == b"FA_ERR_BAD_INDEX"
 
 
-@pytest.mark.parametrize("d,page,Hq", [(64, 16, 80), (128, 128, 70), (96, 256, 200), (256, 48, 30),
+@pytest.mark.parametrize("d,page,Hq", [(64, 16, 80), (128, 128, 70), (96, 256, 200), (256, 48, 80),
                                        (256, 128, 90)])
 def test_bad_pages_with_many_rows(d, page, Hq):
     """A page outside the pool in the middle, found cell by cell or by the tile of keys."""
@@ -715,7 +715,7 @@ def test_stalled_copies_are_reported_and_the_context_survives(d, Nq):
         assert lib.fa_debug_configure(1, 20_000_000) == 0  # no copies, 20 ms a wait
         fa().cache_forward(q.cuda(), c, table.cuda(), ints([500]), causal=True)
         code = status()
-        kernel = 12 if 2 * Nq > 32 else 11
+        kernel = 12 if 2 * Nq > 64 else 11
         assert code & BAD_INDEX == 0x80000000 and (code >> 16) & 0x3FFF == kernel
     finally:
         lib.fa_debug_configure(0, 0)
