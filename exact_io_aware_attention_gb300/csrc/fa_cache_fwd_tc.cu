@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait_all();
         __syncwarp();
         uint32_t top2 = 0;  // the largest magnitudes of the even and the odd channels
-#pragma unroll 4
+#pragma unroll 8
         for (int x = 0; x < D / 8; ++x) {
           uint32_t w[4];
           lds128(at(x), w[0], w[1], w[2], w[3]);
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a row with an infinity or a NaN is NaN throughout: so are its scores)
         const float up = scaled ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
         c_row = (scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f) * p.scale_log2;
-#pragma unroll 2
+#pragma unroll 4
         for (int x = 0; x < D / 8; ++x) {
           uint32_t w[4];
           lds128(at(x), w[0], w[1], w[2], w[3]);
@@ -900,6 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             : !whole ? reinterpret_cast<uint8_t *>(p.part + prow * D)
                      : static_cast<uint8_t *>(p.o) + at * (p.o_f32 ? 4 : 2);
         const uint32_t mine32 = sb + L::kQ + (kNT == 2 ? t : 0) * L::kQBytes + (warp & 3) * 4096;
+        const int piece4 = lane & 7;  // columns 4 piece4 .. of the 32
+        uint8_t *row_to[8];           // of rows 4 y + lane / 8
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          row_to[y] = reinterpret_cast<uint8_t *>(__shfl_sync(
+              0xffffffffu, reinterpret_cast<unsigned long long>(to), 4 * y + (lane >> 3)));
 #pragma unroll 1
         for (int q = 0; q < kG; ++q) {
           uint32_t o[32];
@@ -918,22 +924,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts128(mine32 + lane * 128 + ((x ^ (lane & 7)) << 4), o[4 * x], o[4 * x + 1],
                    o[4 * x + 2], o[4 * x + 3]);
           __syncwarp();
-          const int piece4 = lane & 7;  // columns 4 piece4 .. of the 32
-#pragma unroll 2
+#pragma unroll
           for (int y = 0; y < 8; ++y) {
             const int rr = 4 * y + (lane >> 3);
-            uint8_t *const row_to = reinterpret_cast<uint8_t *>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), rr));
-            uint32_t w[4];
-            lds128(mine32 + rr * 128 + ((piece4 ^ (rr & 7)) << 4), w[0], w[1], w[2], w[3]);
-            if (!row_to) {
-            } else if (wide) {
-              reinterpret_cast<uint4 *>(row_to)[q * 8 + piece4] = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-              reinterpret_cast<uint2 *>(row_to)[q * 8 + piece4] =
-                  make_uint2(pack2<kF16>(__uint_as_float(w[0]), __uint_as_float(w[1])),
-                             pack2<kF16>(__uint_as_float(w[2]), __uint_as_float(w[3])));
-            }
+            lds128(mine32 + rr * 128 + ((piece4 ^ (rr & 7)) << 4), o[4 * y], o[4 * y + 1],
+                   o[4 * y + 2], o[4 * y + 3]);
+          }
+          if (wide) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              if (row_to[y])
+                reinterpret_cast<uint4 *>(row_to[y])[q * 8 + piece4] =
+                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              if (row_to[y])
+                reinterpret_cast<uint2 *>(row_to[y])[q * 8 + piece4] = make_uint2(
+                    pack2<kF16>(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1])),
+                    pack2<kF16>(__uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3])));
           }
         }
         if (store) {
