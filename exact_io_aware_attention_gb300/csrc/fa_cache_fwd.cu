@@ -249,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
     constexpr float kSumScale = kF16 ? 0x1p-6f : 0x1p-24f;  // f16 has no room for 2^-24
     uint32_t qb[NT][kG][4];
     uint32_t qs[NT][2];
+    constexpr bool kThird = D == 256 && !kF16;  // 16 columns hold two terms of eight groups
+    [[maybe_unused]] uint32_t qs3[NT];           // (two of bf16: 2^-17, a third 2^-25)
     float c_row[NT][2];      // score = c_row * (products), in log2 units
     int lim[NT][2];          // visible keys of the row
 #pragma unroll
@@ -317,6 +319,24 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
           word = tt == t ? pair : word;
         }
         qs[nt][half] = word;
+      }
+      if constexpr (kThird) {
+        uint32_t word = 0;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          float a = sum[2 * tt], c = sum[2 * tt + 1];
+          uint32_t pair = 0;
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            float ra, rc;
+            pair = pack2<kF16>(a, c);
+            unpack2<kF16>(pair, ra, rc);
+            a -= ra;
+            c -= rc;
+          }
+          word = tt == t ? pair : word;
+        }
+        qs3[nt] = word;
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -418,6 +438,8 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sc[x2][nt][x] = 0.f;
           mma16816_own<kF16>(sc[x2][nt], la, lb, la, lb, qs[nt][0], qs[nt][1]);
+          if constexpr (kThird)
+            mma16816_own<kF16>(sc[x2][nt], la, lb, 0u, 0u, qs3[nt], 0u);
           if constexpr (kF16)
 #pragma unroll
             for (int x = 0; x < 4; ++x) sc[x2][nt][x] *= 0x1p-18f;

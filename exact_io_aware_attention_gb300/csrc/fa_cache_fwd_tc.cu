@@ -66,13 +66,15 @@ constexpr int kRows = 128;
 constexpr int tile_keys(int d) { return d == 256 ? 64 : 128; }
 constexpr float kRescaleThreshold = 8.0f;  // log2: m moves when P would pass 2^8
 
-template <int D, int kNT>
+template <int D, int kNT, int kTerms>
 struct TcLayout {
   static constexpr int kG = D / 32;
   static constexpr int kKeys = tile_keys(D);
   static constexpr int kChunks = (D + 63) / 64;         // 64-channel chunks of a Q or K row
   static constexpr int kQBytes = kChunks * kRows * 128;  // 128 rows of 128 bytes a chunk
-  static constexpr int kKBytes = kChunks * kKeys * 128;
+  static constexpr int kKBytes = kChunks * kKeys * 128;  // of one term
+  // the groups' sums: 32 bytes a row of Q or K, or 64
+  static constexpr int kXGroups = kG <= 4 ? 4 : 8, kXBytes = kG <= 4 ? 32 : 64;
   static constexpr int kVChunk = D * 128;               // D rows of 64 slots
   static constexpr int kVBytes = kKeys / 64 * kVChunk;
   static constexpr int kPacked = kKeys / kCellTokens * cell_bytes(D);
@@ -81,11 +83,13 @@ struct TcLayout {
   // as soon as both S have been issued, V's only after both P V, a step later
   // (measured with one of V and two of K: 2.5 us a tile, the expansion of V waiting
   // for the products and they for it).
-  static constexpr int kKBufs = kNT == 2 || D == 256 ? 1 : 2;
+  static constexpr int kKBufs = kNT == 2 || D == 256 || kTerms == 2 ? 1 : 2;
   static constexpr int kK = kQ + kNT * kQBytes;           // (kNT = 1: the merge's O later)
-  static constexpr int kV = kK + kKBufs * kKBytes;        // two buffers
+  static constexpr int kV = kK + kKBufs * kTerms * kKBytes;  // two buffers
   static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
-  static constexpr int kMetaK = kRing + 2 * kPacked;      // [g][slot]: (s, s), (lo, lo) in f16
+  static constexpr int kQx = kRing + 2 * kPacked;         // sums of Q, and the middles of K
+  static constexpr int kKx = kQx + kNT * kRows * kXBytes;
+  static constexpr int kMetaK = kKx + kKBufs * kKeys * kXBytes;  // [g][slot]: s's terms in f16, twice
   static constexpr int kMetaV = kMetaK + kKeys * kG * 8;  // [cell][y][g][t]: s, then lo, of two slots
   static constexpr int kVLo = kMetaV + kKeys / 2 * kG * 4;
   static constexpr int kNan = kVLo + kKeys / 2 * kG * 4;  // [4][128] groups of V that are NaN
@@ -133,6 +137,14 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   st_shared_v4(a, x, y, z, w);
 }
@@ -163,6 +175,16 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s2, uint32_t lo2
   else
     u = hadd2((w & 0x000f000fu) | 0x64006400u, 0xe400e400u);               // - 1024
   return hfma2(u, s2, lo2);
+}
+
+// u - 8 of the four pairs of codes of a word, exact.
+template <int kPair>
+__device__ __forceinline__ uint32_t centred(uint32_t w) {
+  if constexpr (kPair >= 2) w >>= 8;
+  if constexpr (kPair & 1)
+    return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u);  // / 16, - 72
+  else
+    return hadd2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u);               // - 1032
 }
 
 // A barrier of kCount threads, and whether all of them are well: they give up
@@ -214,7 +236,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 template <int D, bool kF16, int kNT>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_cache_fwd_tc_kernel(const __grid_constant__ CacheFwdParams p) {
-  using L = TcLayout<D, kNT>;
+  constexpr int kTerms = kF16 ? 2 : 1;
+  using L = TcLayout<D, kNT, kTerms>;
   constexpr int kG = L::kG, kKeys = L::kKeys, kTileCells = kKeys / kCellTokens;
   constexpr int kSCols = 128;           // tensor memory columns of S
   constexpr bool kTurns = kNT == 1 && D != 256;  // the softmax warpgroups take turns at the tiles
@@ -356,14 +379,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = sdesc_sw128(sb + L::kQ, 16, 1024);
         const uint64_t k_desc = sdesc_sw128(sb + L::kK, 16, 1024);
         const uint64_t v_desc = sdesc_sw128(sb + L::kV, 16, 1024);
+        const uint64_t qx_desc = sdesc_plain(sb + L::kQx, 128, 8 * L::kXBytes);
+        const uint64_t kx_desc = sdesc_plain(sb + L::kKx, 128, 8 * L::kXBytes);
         auto issue_s = [&](int t, uint32_t i) {
           const uint64_t q = q_desc + (kNT == 2 ? t : 0) * (L::kQBytes >> 4);
-          const uint64_t k = k_desc + (i % L::kKBufs) * (L::kKBytes >> 4);
+          const uint64_t k = k_desc + (i % L::kKBufs) * (kTerms * L::kKBytes >> 4);
+          const uint64_t qx = qx_desc + (kNT == 2 ? t : 0) * (kRows * L::kXBytes >> 4);
+          const uint64_t kx = kx_desc + (i % L::kKBufs) * (kKeys * L::kXBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < L::kXBytes / 32; ++kk)
+            mma_f16kind_ss(tmem + t * kSCols, qx + kk * 16, kx + kk * 16, kIdS, kk > 0);
+#pragma unroll 1
+          for (int term = 0; term < kTerms; ++term)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const int q_off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
             const int k_off = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
-            mma_f16kind_ss(tmem + t * kSCols, q + q_off, k + k_off, kIdS, kk > 0);
+            mma_f16kind_ss(tmem + t * kSCols, q + q_off, k + term * (L::kKBytes >> 4) + k_off, kIdS, 1u);
           }
           mma_commit(bars.s_full(t));
         };
@@ -410,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // S of tile i for the t whose turn it is
           auto issue_turn = [&](uint32_t i) {
             issue_s(i & 1, i);
-            mma_commit(bars.k_free(i & 1));
+            mma_commit(bars.k_free(i % L::kKBufs));
           };
           if (ok) issue_turn(tile0);
           if (ok && count > 1) {
@@ -456,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 1)));
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
+          uint32_t mid[4] = {0, 0, 0, 0};  // the groups' middles: four f16, and what they lack
           {
             // s and lo of a slot's groups g0 .. g0 + kGp - 1
             const int own = dt % kKeys, g0 = dt / kKeys * kGp, cell = own >> 4;
@@ -494,9 +527,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = tile_exponent(expand_max<1>(top, red, dw));
             const float down = pow2(-e);
 #pragma unroll
-            for (int g = 0; g < kGp; ++g)
-              sts64(sb + L::kMetaK + ((g0 + g) * kKeys + own) * 8, pack_f16x2(s[g] * down, s[g] * down),
-                    pack_f16x2(lo[g] * down, lo[g] * down));
+            for (int g = 0; g < kGp; ++g) {
+              const uint32_t at_s = sb + L::kMetaK + ((g0 + g) * kKeys + own) * (4 * kTerms);
+              const uint32_t s2 = pack_f16x2(s[g] * down, s[g] * down);
+              if constexpr (kTerms == 2) {  // 8 bits, and the rest
+                const uint32_t high = s2 & 0xfff8fff8u;
+                sts64(at_s, high, hadd2(s2, high ^ 0x80008000u));
+              } else {
+                sts32(at_s, s2);
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < (kGp + 1) / 2; ++x) {
+              float m0 = fmaf(8.f, s[2 * x], lo[2 * x]) * (down * 64.f), m1 = 0.f, h0, h1;
+              if (2 * x + 1 < kGp) m1 = fmaf(8.f, s[2 * x + 1], lo[2 * x + 1]) * (down * 64.f);
+              mid[x] = pack_f16x2(m0, m1);
+              unpack2<true>(mid[x], h0, h1);
+              mid[2 + x] = pack_f16x2(m0 - h0, m1 - h1);
+            }
             if (dt == 0) scales[(i & 3) * 4] = pow2(e);
           }
           // the buffer that S of an earlier tile has read
@@ -504,7 +552,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_wait_inl(bars.k_free(i % L::kKBufs), ((i / L::kKBufs) & 1) ^ 1, st,
                             code(kRoleExpand, 2)));
           if (!ok) break;
-          const uint32_t dst = sb + L::kK + (i % L::kKBufs) * L::kKBytes;
+          {
+            const int own = dt % kKeys, part = dt / kKeys;
+            const uint32_t at = sb + L::kKx + (i % L::kKBufs) * (kKeys * L::kXBytes) +
+                                (own >> 3) * (8 * L::kXBytes) + (own & 7) * 16;
+            if constexpr (L::kXGroups == 4) {
+              sts128(at, mid[0], mid[1], mid[0], mid[1]);
+              sts128(at + 128, mid[2], mid[3], 0u, 0u);
+            } else {
+              sts64(at + part * 8, mid[0], mid[1]);
+              sts64(at + 128 + part * 8, mid[0], mid[1]);
+              sts64(at + 256 + part * 8, mid[2], mid[3]);
+              sts64(at + 384 + part * 8, 0u, 0u);
+            }
+          }
+          const uint32_t dst = sb + L::kK + (i % L::kKBufs) * (kTerms * L::kKBytes);
           // eight lanes that load and store together: the four t, and two slots that
           // differ in bit 0 (words of other banks) and in bit 2 (pieces of other banks)
           const int t = lane & 3, low = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
@@ -519,12 +581,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < kGp; ++y) {
               const int g = g0 + y;
-              uint32_t s2, lo2;
-              lds64(sb + L::kMetaK + (g * kKeys + slot) * 8, s2, lo2);
+              uint32_t s2[2];
+              if constexpr (kTerms == 2)
+                lds64(sb + L::kMetaK + (g * kKeys + slot) * 8, s2[0], s2[1]);
+              else
+                s2[0] = lds32(sb + L::kMetaK + (g * kKeys + slot) * 4);
               const int block = (g & 1) * 4 + t;
-              sts128(dst + (g >> 1) * (kKeys * 128) + slot * 128 + ((block ^ (slot & 7)) << 4),
-                     expand<0>(w[y], s2, lo2), expand<1>(w[y], s2, lo2), expand<2>(w[y], s2, lo2),
-                     expand<3>(w[y], s2, lo2));
+              const uint32_t v0 = centred<0>(w[y]), v1 = centred<1>(w[y]);
+              const uint32_t v2 = centred<2>(w[y]), v3 = centred<3>(w[y]);
+#pragma unroll
+              for (int term = 0; term < kTerms; ++term)
+                sts128(dst + term * L::kKBytes + (g >> 1) * (kKeys * 128) + slot * 128 +
+                           ((block ^ (slot & 7)) << 4),
+                       hmul2(v0, s2[term]), hmul2(v1, s2[term]), hmul2(v2, s2[term]),
+                       hmul2(v3, s2[term]));
             }
           }
           fence_proxy_async_smem();
@@ -687,19 +757,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a row with an infinity or a NaN is NaN throughout: so are its scores)
         const float up = scaled ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
         c_row = (scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f) * p.scale_log2;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {
-          uint32_t w[4];
-          lds128(at(x), w[0], w[1], w[2], w[3]);
-          float q[8];
+        // and the sums of its groups, as two f16 terms each, for the middles of K
+        const uint32_t sums = sb + L::kQx + (kNT == 2 ? t : 0) * (kRows * L::kXBytes) +
+                              (r >> 3) * (8 * L::kXBytes) + (r & 7) * 16;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) unpack2<kF16>(w[y], q[2 * y], q[2 * y + 1]);
+        for (int x = 0; x < L::kXBytes / 16; ++x) sts128(sums + x * 128, 0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int g = 0; g < kG; ++g) {
+          float sum = 0.f;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            w[y] = pack_f16x2(q[y] * up, q[y + 4] * up);
-            if (!finite) w[y] = 0x7fff7fffu;
+          for (int x = 4 * g; x < 4 * g + 4; ++x) {
+            uint32_t w[4];
+            lds128(at(x), w[0], w[1], w[2], w[3]);
+            float q[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              unpack2<kF16>(w[y], q[2 * y], q[2 * y + 1]);
+              sum += q[2 * y] * up + q[2 * y + 1] * up;
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              w[y] = pack_f16x2(q[y] * up, q[y + 4] * up);
+              if (!finite) w[y] = 0x7fff7fffu;
+            }
+            sts128(at(x), w[0], w[1], w[2], w[3]);
           }
-          sts128(at(x), w[0], w[1], w[2], w[3]);
+          sum = finite ? sum * 0x1p-6f : 0.f;
+          float high, unused;
+          const uint32_t sum_high = pack_f16x2(sum, 0.f);
+          unpack2<true>(sum_high, high, unused);
+          auto put = [&](int column, uint32_t x) {
+            sts16(sums + (column >> 3) * 128 + (column & 7) * 2, x);
+          };
+          put(g, sum_high);
+          put(L::kXGroups + g, pack_f16x2(sum - high, 0.f));
+          put(2 * L::kXGroups + g, sum_high);
         }
         if (kTurns) row_scale[r] = c_row;
         fence_proxy_async_smem();
@@ -967,31 +1059,33 @@ template <int D, bool kF16, int kNT>
 cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
   static std::atomic<bool> configured[64];  // per device
   const cudaError_t e =
-      allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16, kNT>, TcLayout<D, kNT>::kAlloc, configured);
+      allow_shared_memory(fa_cache_fwd_tc_kernel<D, kF16, kNT>, TcLayout<D, kNT, kF16 ? 2 : 1>::kAlloc, configured);
   if (e != cudaSuccess) return e;
   static const cudaError_t regs = check_kernel_regs(fa_cache_fwd_tc_kernel<D, kF16, kNT>, kRegsLaunch);
   if (regs != cudaSuccess) return regs;
   LaunchProbe probe(kKindCacheFwdTc, stream);
-  fa_cache_fwd_tc_kernel<D, kF16, kNT><<<p.ctas, kThreads, TcLayout<D, kNT>::kAlloc, stream>>>(p);
+  fa_cache_fwd_tc_kernel<D, kF16, kNT><<<p.ctas, kThreads, TcLayout<D, kNT, kF16 ? 2 : 1>::kAlloc, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool kF16>
-cudaError_t launch_tc_rows(const CacheFwdParams &p, bool two, cudaStream_t stream) {
-  if constexpr (D != 256)
-    if (two) return launch_tc<D, kF16, 2>(p, stream);
-  return launch_tc<D, kF16, 1>(p, stream);
+template <int D>
+cudaError_t launch_tc_rows(const CacheFwdParams &p, cudaStream_t stream) {
+  if constexpr (D == 256) {
+    return p.pool.f16 ? cudaErrorInvalidValue : launch_tc<D, false, 1>(p, stream);
+  } else {
+    if (p.pool.f16) return launch_tc<D, true, 1>(p, stream);
+    return p.block_rows == 256 ? launch_tc<D, false, 2>(p, stream) : launch_tc<D, false, 1>(p, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_forward_tc(const CacheFwdParams &p, cudaStream_t stream) {
-  const bool f16 = p.pool.f16 != 0, two = p.block_rows == 256;
   switch (p.pool.d) {
-    case 64: return f16 ? launch_tc_rows<64, true>(p, two, stream) : launch_tc_rows<64, false>(p, two, stream);
-    case 96: return f16 ? launch_tc_rows<96, true>(p, two, stream) : launch_tc_rows<96, false>(p, two, stream);
-    case 128: return f16 ? launch_tc_rows<128, true>(p, two, stream) : launch_tc_rows<128, false>(p, two, stream);
-    case 256: return f16 ? launch_tc_rows<256, true>(p, two, stream) : launch_tc_rows<256, false>(p, two, stream);
+    case 64: return launch_tc_rows<64>(p, stream);
+    case 96: return launch_tc_rows<96>(p, stream);
+    case 128: return launch_tc_rows<128>(p, stream);
+    case 256: return launch_tc_rows<256>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

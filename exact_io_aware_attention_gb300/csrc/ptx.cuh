@@ -290,6 +290,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same without swizzle, K-major: 8 rows of 16 bytes lie together (128 bytes);
+// the next 16 bytes of the rows are `lbo` bytes on, the next 8 rows `sbo`.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05: tensor memory <-> registers. Shape 32x32b: warp w (w % 4 = q)
 // reaches lanes 32q..32q+31; thread t of the warp gets lane 32q+t, and .xN
