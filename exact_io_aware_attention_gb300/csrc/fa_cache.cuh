@@ -188,7 +188,7 @@ constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 // Query rows (new tokens times query heads of one K/V head) that one CTA
 // holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
 // tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
-// (d = 256, f16: 128; both: never) in the one for many.
+// (d = 256 and f16: 128) in the one for many.
 //
 // Up to 64 rows few: the other kernel needs 8 to 15 us more before and after its
 // tiles, which only much work outweighs. Measured (few / many, whole calls), 4
@@ -205,7 +205,7 @@ constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 constexpr int cache_forward_block_rows(int d, bool f16, long long rows, bool whole, double heads,
                                        int sms) {
   const int few = d == 256 || rows <= 8 ? 8 : 16;
-  if (rows <= 64 || (f16 && d == 256)) return few;
+  if (rows <= 64) return few;
   if (whole && heads * ((rows + few - 1) / few) <=
                    (d == 256 ? 2.0 : 1.0) * sms * cache_forward_ctas_per_sm(d, few))
     return few;

@@ -86,7 +86,8 @@ struct TcLayout {
   static constexpr int kKBufs = kNT == 2 || D == 256 || kTerms == 2 ? 1 : 2;
   static constexpr int kK = kQ + kNT * kQBytes;           // (kNT = 1: the merge's O later)
   static constexpr int kV = kK + kKBufs * kTerms * kKBytes;  // two buffers
-  static constexpr int kRing = kV + 2 * kVBytes;          // two tiles of cells
+  static constexpr int kVBufs = D == 256 && kTerms == 2 ? 1 : 2;
+  static constexpr int kRing = kV + kVBufs * kVBytes;     // two tiles of cells
   static constexpr int kQx = kRing + 2 * kPacked;         // sums of Q, and the middles of K
   static constexpr int kKx = kQx + kNT * kRows * kXBytes;
   static constexpr int kMetaK = kKx + kKBufs * kKeys * kXBytes;  // [g][slot]: s's terms in f16, twice
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(bars.s_full(t));
         };
         auto issue_pv = [&](int t, uint32_t i, bool first) {
-          const uint64_t v = v_desc + (i & 1) * (L::kVBytes >> 4);
+          const uint64_t v = v_desc + (i % L::kVBufs) * (L::kVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
             mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kSCols + kk * 8,
@@ -615,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // softmax has then seen its own scales: their barrier has two places)
           ok = expand_sync<2>(
               ok && mbar_wait_inl(bars.packed_full(slot2), parity, st, code(kRoleExpand, 3)) &&
-              mbar_wait_inl(bars.v_free(slot2), parity ^ 1, st, code(kRoleExpand, 4)));
+              (L::kVBufs == 1 ||
+               mbar_wait_inl(bars.v_free(slot2), parity ^ 1, st, code(kRoleExpand, 4))));
           if (!ok) break;
           const uint32_t found = (uint32_t)found_cells[i & 3];
           {
@@ -660,8 +662,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mbar_arrive(bars.v_scale(slot2));
-          expand_sync<2>(true);
-          const uint32_t dst = sb + L::kV + slot2 * L::kVBytes;
+          // (one buffer: P V of the last tile has read it)
+          ok = expand_sync<2>(L::kVBufs == 2 ||
+                              mbar_wait_inl(bars.v_free(slot2 ^ 1), ((i - 1) >> 1) & 1, st,
+                                            code(kRoleExpand, 4)));
+          if (!ok) break;
+          const uint32_t dst = sb + L::kV + (i % L::kVBufs) * L::kVBytes;
           // eight lanes that store together: four blocks of 8 slots, two r
           const int kb = (lane & 3) | (dw % (kKeys / 32) << 2);  // block of 8 slots: cell * 2 + y
           const int g0 = dw / (kKeys / 32) * kGp;
@@ -1070,12 +1076,10 @@ cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_tc_rows(const CacheFwdParams &p, cudaStream_t stream) {
-  if constexpr (D == 256) {
-    return p.pool.f16 ? cudaErrorInvalidValue : launch_tc<D, false, 1>(p, stream);
-  } else {
-    if (p.pool.f16) return launch_tc<D, true, 1>(p, stream);
-    return p.block_rows == 256 ? launch_tc<D, false, 2>(p, stream) : launch_tc<D, false, 1>(p, stream);
-  }
+  if (p.pool.f16) return launch_tc<D, true, 1>(p, stream);
+  if constexpr (D != 256)
+    if (p.block_rows == 256) return launch_tc<D, false, 2>(p, stream);
+  return launch_tc<D, false, 1>(p, stream);
 }
 
 }  // namespace
