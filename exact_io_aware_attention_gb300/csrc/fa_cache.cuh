@@ -209,7 +209,7 @@ constexpr int cache_forward_block_rows(int d, bool f16, long long rows, bool who
   if (whole && heads * ((rows + few - 1) / few) <=
                    (d == 256 ? 2.0 : 1.0) * sms * cache_forward_ctas_per_sm(d, few))
     return few;
-  return f16 || d == 256 || rows <= 128 || (whole && heads * ((rows + 127) / 128) <= sms) ? 128 : 256;
+  return d == 256 || rows <= 128 || (whole && heads * ((rows + 127) / 128) <= sms) ? 128 : 256;
 }
 
 }  // namespace fa

@@ -86,7 +86,7 @@ struct TcLayout {
   static constexpr int kKBufs = kNT == 2 || D == 256 || kTerms == 2 ? 1 : 2;
   static constexpr int kK = kQ + kNT * kQBytes;           // (kNT = 1: the merge's O later)
   static constexpr int kV = kK + kKBufs * kTerms * kKBytes;  // two buffers
-  static constexpr int kVBufs = D == 256 && kTerms == 2 ? 1 : 2;
+  static constexpr int kVBufs = kTerms == 2 && kNT * D >= 256 ? 1 : 2;
   static constexpr int kRing = kV + kVBufs * kVBytes;     // two tiles of cells
   static constexpr int kQx = kRing + 2 * kPacked;         // sums of Q, and the middles of K
   static constexpr int kKx = kQx + kNT * kRows * kXBytes;
@@ -1076,10 +1076,10 @@ cudaError_t launch_tc(const CacheFwdParams &p, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_tc_rows(const CacheFwdParams &p, cudaStream_t stream) {
-  if (p.pool.f16) return launch_tc<D, true, 1>(p, stream);
+  const bool f16 = p.pool.f16 != 0;
   if constexpr (D != 256)
-    if (p.block_rows == 256) return launch_tc<D, false, 2>(p, stream);
-  return launch_tc<D, false, 1>(p, stream);
+    if (p.block_rows == 256) return f16 ? launch_tc<D, true, 2>(p, stream) : launch_tc<D, false, 2>(p, stream);
+  return f16 ? launch_tc<D, true, 1>(p, stream) : launch_tc<D, false, 1>(p, stream);
 }
 
 }  // namespace
