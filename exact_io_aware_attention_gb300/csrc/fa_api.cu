@@ -8,7 +8,6 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <vector>
@@ -604,11 +603,11 @@ struct CacheScratch {
   int ctas, block_rows;
   size_t part, lse, chain;
 };
-bool cache_scratch(int sms, int B, int Hq, int Hk, int Nq, int d, bool f16, long long tokens,
+bool cache_scratch(int sms, int B, int Hq, int Hk, int Nq, int d, long long tokens,
                    CacheScratch *out) {
   if (sms <= 0 || Hk <= 0) return false;
   const int block_rows = out->block_rows = fa::cache_forward_block_rows(
-      d, f16, (long long)(Hq / Hk) * Nq, fa::cache_forward_whole(tokens), (double)B * Hk, sms);
+      d, (long long)(Hq / Hk) * Nq, fa::cache_forward_whole(tokens), (double)B * Hk, sms);
   out->ctas = sms * fa::cache_forward_ctas_per_sm(d, block_rows);
   const size_t rows = (size_t)out->ctas * 2 * block_rows;
   out->part = round_up(rows * d * sizeof(float));
@@ -651,7 +650,7 @@ fa_status cache_forward_impl(const fa_tensor *Q, const fa_cache *cache, const in
     return FA_ERR_MISALIGNED;
   if ((s = bind_device(cache->data)) != FA_OK) return s;
   CacheScratch w;
-  if (!cache_scratch(sm_count(), B, Hq, cache->heads, Nq, d, cache->dtype == FA_F16, tokens, &w))
+  if (!cache_scratch(sm_count(), B, Hq, cache->heads, Nq, d, tokens, &w))
     return cuda_fail("SM count", cudaErrorInvalidDevice);
   if (ws_bytes < w.part + w.lse + w.chain) {
     snprintf(g_last_error, sizeof(g_last_error), "workspace of %zu bytes, %zu needed", ws_bytes,
@@ -972,11 +971,7 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
 size_t fa_cache_forward_workspace_bytes(int Hq, int Hk, int Nq, int d, int max_tokens) {
   if (Hq < 0 || Hk <= 0 || Nq < 0 || max_tokens < 0 || (d != 64 && d != 96 && d != 128 && d != 256)) return 0;
   CacheScratch w;
-  size_t most = 0;
-  for (bool f16 : {false, true})
-    if (cache_scratch(sm_count(), 1, Hq, Hk, Nq, d, f16, max_tokens, &w))
-      most = std::max(most, w.part + w.lse + w.chain);
-  return most;
+  return cache_scratch(sm_count(), 1, Hq, Hk, Nq, d, max_tokens, &w) ? w.part + w.lse + w.chain : 0;
 }
 
 fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,

@@ -188,7 +188,7 @@ constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 // Query rows (new tokens times query heads of one K/V head) that one CTA
 // holds: 8 or 16 in the kernel for few rows, whose product has 8 columns a
 // tile (d = 256: 8, two tiles' outputs would not fit the registers), 128 or 256
-// (d = 256 and f16: 128) in the one for many.
+// (d = 256: 128) in the one for many.
 //
 // Up to 64 rows few: the other kernel needs 8 to 15 us more before and after its
 // tiles, which only much work outweighs. Measured (few / many, whole calls), 4
@@ -202,8 +202,7 @@ constexpr bool cache_forward_whole(long long tokens) { return tokens <= 1024; }
 // as long as they do. Measured, up to 1000 keys, d = 128 (few / many): 8 heads
 // of 512 rows, 256 segments, 23 / 36 us; 64 heads of 128 rows, 512 segments,
 // 38 / 28 us; 12 heads of 1000 rows (128 / 256 rows a CTA) 27 / 36 us.
-constexpr int cache_forward_block_rows(int d, bool f16, long long rows, bool whole, double heads,
-                                       int sms) {
+constexpr int cache_forward_block_rows(int d, long long rows, bool whole, double heads, int sms) {
   const int few = d == 256 || rows <= 8 ? 8 : 16;
   if (rows <= 64) return few;
   if (whole && heads * ((rows + few - 1) / few) <=

@@ -1,17 +1,23 @@
 // Attention over the 4-bit K/V cache for many query rows (a chunk of a prompt,
-// drafted tokens times the query heads of a K/V head): 128 rows a CTA on
+// drafted tokens times the query heads of a K/V head): 128 or 256 rows a CTA on
 // tcgen05, O = softmax(scale Q K^T) V with K and V expanded in shared memory.
 //
 // With this many rows the products no longer fit the time that the codes take
 // to arrive, so they run on tcgen05, whose operands are 16-bit values: a tile
-// of 128 keys is expanded once for all 128 rows, K^ = lo + s u and V^ likewise,
-// rounded once to f16. What is f16 in bf16 caches too: f16 has three bits more
-// than bf16, and a power of two for each tile (2^eK, 2^eV over its largest
-// |lo|, |lo + 15 s|) takes the place of bf16's exponents: the scores are
-// multiplied with 2^eK in fp32, and the weights P carry 2^eV. The running
-// reference m follows max_j (score_j + eV), so P stays below 2^8 and the
-// accumulators have one scale. Roundings: K^, V^, P 2^-11 relative each (K^ and
-// V^ of elements below 2^-22 of a tile's largest: 2^-25 of 2^-15 of that).
+// of 128 keys (d = 256: 64) is expanded once for all rows of a CTA. The operands
+// are f16 for bf16 caches too: f16 has three bits more than bf16, and a power of
+// two for each tile (2^eK, 2^eV over its largest |lo|, |lo + 15 s|) takes the
+// place of bf16's exponents: the scores are multiplied with 2^eK in fp32, and the
+// weights P carry 2^eV. The running reference m follows max_j (score_j + eV), so P
+// stays below 2^8 and the accumulators have one scale.
+//   K: an error of a score is one of its weight, and of the log-sum-exp, so K is
+//      not rounded: K = mid + s (u - 8), mid = lo + 8 s, and the operand is
+//      s (u - 8), which fits f16's 11 bits for the 8 bits of a bf16 s; an f16 s is
+//      cut into 8 bits and the rest, two operands (the chunk below: 222 -> 269 us).
+//      mid meets only the sums of q over its group: a product of 16 columns (32
+//      for d = 256), mid and the sums as two f16 terms each.
+//   V^ = lo + s u is rounded once to f16, as P is: 2^-11 relative each (V^ of
+//      elements below 2^-22 of a tile's largest: 2^-25 of 2^-15 of that).
 //
 // The order of the operands is that in which the cache holds its codes, so
 // that they are stored to shared memory as they come out of the words:
@@ -32,7 +38,8 @@
 // The two softmax warpgroups take turns with the tensor cores, either (kNT = 2,
 // more than 128 rows a K/V head) on 128 rows each, which share every expanded
 // tile, or (kNT = 1) on the same 128 rows and every second tile of keys each,
-// with an m, l and O of their own that they merge at the end.
+// with an m, l and O of their own that they merge at the end. With d = 256 there
+// is tensor memory for one O only, and the second warpgroup is idle.
 // Tensor memory: S_t [128 t, +128), P_t over the first 64 of these columns once
 // they have been read, O_t [256 + t d, +d). The issue order P_t V, next S_t, per
 // t, makes the completion of S_t tell that O_t and P_t are free.
@@ -42,10 +49,13 @@
 // and rows that see the token remember the group and put NaN in its channels
 // at the end. A NaN in K needs no such care: hidden scores are overwritten.
 // Measured (GB300): 2 sequences of 9000 and 16384 keys, 1024 new tokens each, 16
-// query heads on 4, d = 128: 243 us and the merge, 280 us in all (the kernel for few
-// rows: 1020 us), 0.76 PFLOP/s, the tensor pipe 39 % active. A tile of 128 keys for
-// 256 rows takes 2.2 us: two expansions of 1.4 us side by side, two softmaxes of
-// 1.4 us, all four sharing the schedulers (0.49 instructions a cycle each).
+// query heads on 4, d = 128: 222 us, with the merge 232 us a call (the kernel for few
+// rows: 1020 us), 0.96 PFLOP/s. A tile of 128 keys for 256 rows takes 2 us: two
+// expansions side by side and two softmaxes share the schedulers. What a piece
+// needs besides its tiles, about 10 us the first time, was as much in fetching
+// instructions that run once as in their work: their loops are kept short.
+// d = 256, 2 sequences of 6000 and 9000 keys, 2048 rows on each of 2 heads: 121 us
+// (f16 144 us; the kernel for few rows 359 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -82,10 +92,10 @@ struct TcLayout {
   // Buffers of K and V tiles: with 256 rows there is room for three. K's is free
   // as soon as both S have been issued, V's only after both P V, a step later
   // (measured with one of V and two of K: 2.5 us a tile, the expansion of V waiting
-  // for the products and they for it).
+  // for the products and they for it). With two terms of K, one of V at d = 128.
   static constexpr int kKBufs = kNT == 2 || D == 256 || kTerms == 2 ? 1 : 2;
   static constexpr int kK = kQ + kNT * kQBytes;           // (kNT = 1: the merge's O later)
-  static constexpr int kV = kK + kKBufs * kTerms * kKBytes;  // two buffers
+  static constexpr int kV = kK + kKBufs * kTerms * kKBytes;
   static constexpr int kVBufs = kTerms == 2 && kNT * D >= 256 ? 1 : 2;
   static constexpr int kRing = kV + kVBufs * kVBytes;     // two tiles of cells
   static constexpr int kQx = kRing + 2 * kPacked;         // sums of Q, and the middles of K
@@ -393,11 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int term = 0; term < kTerms; ++term)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int q_off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
-            const int k_off = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
-            mma_f16kind_ss(tmem + t * kSCols, q + q_off, k + term * (L::kKBytes >> 4) + k_off, kIdS, 1u);
-          }
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int q_off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+              const int k_off = ((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4;
+              mma_f16kind_ss(tmem + t * kSCols, q + q_off, k + term * (L::kKBytes >> 4) + k_off,
+                             kIdS, 1u);
+            }
           mma_commit(bars.s_full(t));
         };
         auto issue_pv = [&](int t, uint32_t i, bool first) {
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // eight lanes that load and store together: the four t, and two slots that
           // differ in bit 0 (words of other banks) and in bit 2 (pieces of other banks)
           const int t = lane & 3, low = (lane >> 3) ^ (((lane >> 2) & 1) * 5);
-// (loops of the roles stay rolled: together they are more code than the
+          // (loops of the roles stay rolled: together they are more code than the
           // instruction cache holds; measured 12 % on a chunk of 1024 tokens)
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {

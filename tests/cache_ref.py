@@ -14,11 +14,13 @@ comes with bounds on the rounding errors of the library's kernels:
   * the result is rounded to the output's type: half a step, eps / 2.
 
 With more than 64 query rows a K/V head there is another kernel, for some of the
-sizes, and the bound is the larger one. In it K, V and P are f16
-operands of the tensor cores: half a step is 2^-11 of each value (of K and V,
-scaled by a power of two to below 2^8 a tile of keys, 2^-25 below f16's normal
-range, so 2^-32 of the tile's largest; of P, whose largest is at least 1, 2^-25).
-An error of 2^-11 of each k_c makes one of 2^-11 scale sum |q_c k_c| of a score.
+sizes, and the bound is the larger one. In it V and P are f16 operands of the tensor
+cores: half a step is 2^-11 of each value (of V, scaled by a power of two to below 2^8
+a tile of keys, 2^-25 below f16's normal range, so 2^-32 of the tile's largest; of P,
+whose largest is at least 1, 2^-25). K is the middle of a group, lo + 8 s, and
+s (u - 8), which is exact but below f16's normal range (2^-31 of the tile's largest);
+the middle and the sums of q that it meets have two f16 terms each, 2^-21 of the
+product in all.
 """
 import numpy as np
 import torch
@@ -93,8 +95,9 @@ def attend(q, k, v, n, causal, scale, out_eps):
                 tO[hq, i] = (2.0 ** -11 * w.sum(0) + m * 2.0 ** -25 * w.max() +
                              2 * rel * (p @ (np.abs(vd[:m]) + 2 * vstep[:m])))
                 if f16_operands:
-                    av, ak = np.abs(vd[:m]), np.abs(kd[:m])
-                    ek = scale * ((2.0 ** -11 * ak + 2.0 ** -32 * ak.max()) @ np.abs(qd[i])).max()
+                    av = np.abs(vd[:m])
+                    ek = scale * ((2.0 ** -21 * kmag[:m] + 2.0 ** -30 * kmag[:m].max()) @
+                                  np.abs(qd[i])).max()
                     rel += 2 * ek
                     tl[hq, i] = ek
                     tO[hq, i] = np.maximum(
