@@ -16,8 +16,10 @@
 //      cut into 8 bits and the rest, two operands (the chunk below: 222 -> 269 us).
 //      mid meets only the sums of q over its group: a product of 16 columns (32
 //      for d = 256), mid and the sums as two f16 terms each.
-//   V^ = lo + s u is rounded once to f16, as P is: 2^-11 relative each (V^ of
-//      elements below 2^-22 of a tile's largest: 2^-25 of 2^-15 of that).
+//   V^ = lo + s u is rounded once to f16, 2^-11 relative (of elements below 2^-22
+//      of a tile's largest: 2^-25 of 2^-15 of that), and P for bf16 caches, whose
+//      outputs are rounded to eight bits; for f16 P has two terms (269 -> 313 us;
+//      O is off by 0.00028 relative against 0.00034, 0.00021 of it its own rounding).
 //
 // The order of the operands is that in which the cache holds its codes, so
 // that they are stored to shared memory as they come out of the words:
@@ -40,8 +42,8 @@
 // tile, or (kNT = 1) on the same 128 rows and every second tile of keys each,
 // with an m, l and O of their own that they merge at the end. With d = 256 there
 // is tensor memory for one O only, and the second warpgroup is idle.
-// Tensor memory: S_t [128 t, +128), P_t over the first 64 of these columns once
-// they have been read, O_t [256 + t d, +d). The issue order P_t V, next S_t, per
+// Tensor memory: S_t [128 t, +128), P_t over the first 64 of these columns (f16: all)
+// once they have been read, O_t [256 + t d, +d). The issue order P_t V, next S_t, per
 // t, makes the completion of S_t tell that O_t and P_t are free.
 //
 // NaN. A group of V with a non-finite element reads as NaN, but 0 times NaN
@@ -55,7 +57,7 @@
 // needs besides its tiles, about 10 us the first time, was as much in fetching
 // instructions that run once as in their work: their loops are kept short.
 // d = 256, 2 sequences of 6000 and 9000 keys, 2048 rows on each of 2 heads: 121 us
-// (f16 144 us; the kernel for few rows 359 us).
+// (f16 170 us; the kernel for few rows 359 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -66,8 +68,8 @@ namespace {
 
 constexpr int kThreads = 640;
 // registers a thread: at the launch, and after the warpgroups have moved them
-// (the softmax holds half a row of scores and reads them twice, for the
-// maximum and for P)
+// (the softmax holds 32 scores of a row at a time and reads them twice, for the
+// maximum and for P; the output's rows are 32 columns at a time too)
 constexpr int kRegsLaunch = 96, kRegsIssue = 48, kRegsSoftmax = 128, kRegsExpand = 88;
 static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand == 5 * kRegsLaunch, "register split");
 static_assert(kRegsLaunch * kThreads <= 65536, "registers of an SM");
@@ -415,9 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t v = v_desc + (i % L::kVBufs) * (L::kVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_f16kind_ts(tmem + 256 + t * D, tmem + t * kSCols + kk * 8,
-                           v + (((kk >> 2) * L::kVChunk + (kk & 3) * 32) >> 4), kIdPV,
-                           (!first || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term)
+              mma_f16kind_ts(tmem + 256 + t * D,
+                             tmem + t * kSCols +
+                                 (kTerms == 1 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8 + term * 16),
+                             v + (((kk >> 2) * L::kVChunk + (kk & 3) * 32) >> 4), kIdPV,
+                             (!first || kk > 0 || term > 0) ? 1u : 0u);
           mma_commit(bars.pv_done(t));
         };
         auto k_here = [&](uint32_t i) {
@@ -889,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x32[32];
           tmem_ld32(tS + q * 32, x32);
           tmem_wait_ld();
-          uint32_t pk[16];
+          uint32_t pk[16 * kTerms];  // (f16: what the first sixteen lack in the others)
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float a, b;
@@ -900,8 +906,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             b = ex2_approx(b);
             sum[x & 1] = fadd2(sum[x & 1], f2pack(a, b));
             pk[x] = pack_f16x2(a, b);
+            if constexpr (kTerms == 2) {
+              float a0, b0;
+              unpack2<true>(pk[x], a0, b0);
+              f2unpack(fsub2(f2pack(a, b), f2pack(a0, b0)), a, b);
+              pk[16 + x] = pack_f16x2(a, b);
+            }
           }
-          tmem_st16(tS + 16 * q, pk);
+          if constexpr (kTerms == 2)
+            tmem_st32(tS + 32 * q, pk);
+          else
+            tmem_st16(tS + 16 * q, pk);
         }
         float la, lb;
         f2unpack(fadd2(sum[0], sum[1]), la, lb);

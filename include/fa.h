@@ -372,15 +372,16 @@ fa_status fa_cache_read(const fa_cache *cache, const fa_tensor *K, const fa_tens
  * NaN among K or V reaches only the rows that see it (V: only its group's
  * channels). B * Hq * Nq <= 2^30 - 1.
  *
- * Up to 64 query rows a cached head (Nq * Hq / heads; any number at d = 256)
- * the codes are multiplied as they are and s, lo applied in fp32; the weights
- * p s are rounded to f16. With more rows K, V and P are rounded to f16 operands
- * (under a power of two for each tile of 128 keys). Sums are fp32 in both.
+ * The scores are exact but for fp32 sums. Up to 64 query rows a cached head (Nq *
+ * Hq / heads), and with more where short sequences do not fill the GPU, the codes
+ * of V are multiplied as they are and the weights p s are rounded to f16. With
+ * more rows V is rounded to f16 (under a power of two for each tile of 128 keys),
+ * and the weights p to f16 for a bf16 cache.
  *
  * The workspace (fa_cache_forward_workspace_bytes, 256-byte aligned; NULL
  * where that is 0) holds partial results while the call runs; calls that may
- * overlap on the GPU need one each. Results do not depend on timing: equal calls on equal GPUs give
- * equal bits.
+ * overlap on the GPU need one each. Results do not depend on timing: equal calls
+ * on equal GPUs give equal bits.
  */
 fa_status fa_cache_forward(const fa_tensor *Q, const fa_cache *cache, const int32_t *page_table,
                            int64_t table_stride, int max_pages, const int32_t *lengths,
