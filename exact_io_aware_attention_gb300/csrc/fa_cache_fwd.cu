@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
     uint32_t qs[NT][2];
     constexpr bool kThird = D == 256 && !kF16;  // 16 columns hold two terms of eight groups
     [[maybe_unused]] uint32_t qs3[NT];           // (two of bf16: 2^-17, a third 2^-25)
-    float c_row[NT][2];      // score = c_row * (products), in log2 units
+    float c_row[NT][2];      // score = 2^24 c_row * (products), in log2 units
     int lim[NT][2];          // visible keys of the row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4) * p.scale_log2 * 0x1p24f;
+        c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4) * p.scale_log2;
         const int tk = p.by_group.div(row0 + nt * 8 + 2 * t + y);
         lim[nt][y] = p.causal && tk < n ? len - n + tk + 1 : len;
       }
@@ -469,13 +469,15 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
           }
         }
         // (rounded before m is taken off: with one rounding for both, a score
-        // beyond 2^24 could come out above the m that it set)
+        // beyond 2^24 could come out above the m that it set; 2^24 by itself: its
+        // product with c_row overflows for q beyond 2^116)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; x += 2)
-            f2unpack(fmul2(f2pack(sc[x2][nt][x], sc[x2][nt][x + 1]),
-                           f2pack(c_row[nt][0], c_row[nt][1])),
+            f2unpack(fmul2(fmul2(f2pack(sc[x2][nt][x], sc[x2][nt][x + 1]),
+                                 f2pack(c_row[nt][0], c_row[nt][1])),
+                           f2pack(0x1p24f, 0x1p24f)),
                      sc[x2][nt][x], sc[x2][nt][x + 1]);
         load_own_token(cell + v_s<D>(0, 0, 0), va[x2], vb[x2]);
         if constexpr (kMasked) {
