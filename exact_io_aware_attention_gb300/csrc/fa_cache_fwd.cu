@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
     uint32_t qs[NT][2];
     constexpr bool kThird = D == 256 && !kF16;  // 16 columns hold two terms of eight groups
     [[maybe_unused]] uint32_t qs3[NT];           // (two of bf16: 2^-17, a third 2^-25)
-    float c_row[NT][2];      // score = 2^24 c_row * (products), in log2 units
+    float c_row[NT][2];      // score = (products * c_row) * (2^24 scale), in log2 units
     int lim[NT][2];          // visible keys of the row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
       finite = __shfl_xor_sync(0xffffffffu, (int)finite, 1) && finite;
       finite = __shfl_xor_sync(0xffffffffu, (int)finite, 2) && finite;
       // 2^(e - 127) <= big < 2^(e - 126), e its exponent field: q * up is below 2^11
-      const int e = max((int)(__float_as_uint(big) >> 23), 40);
+      const int e = max((int)(__float_as_uint(big) >> 23), 11);  // (back is a normal number)
       const float up = big > 0.f && finite ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
       const float back = big > 0.f && finite ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f;
       float sum[kGp] = {};
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
       }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4) * p.scale_log2;
+        c_row[nt][y] = __shfl_sync(0xffffffffu, back, (2 * t + y) * 4);
         const int tk = p.by_group.div(row0 + nt * 8 + 2 * t + y);
         lim[nt][y] = p.causal && tk < n ? len - n + tk + 1 : len;
       }
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
     float acc_g[NT][4];
     uint64_t acc_lo[NT][2][kF16 ? kG : 1];
     float m[NT][2], l[NT][2];
+    const float scale24 = p.scale_log2 * 0x1p24f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -469,15 +470,15 @@ __global__ void __launch_bounds__(kThreads, cache_forward_ctas_per_sm(D, 8 * NT)
           }
         }
         // (rounded before m is taken off: with one rounding for both, a score
-        // beyond 2^24 could come out above the m that it set; 2^24 by itself: its
-        // product with c_row overflows for q beyond 2^116)
+        // beyond 2^24 could come out above the m that it set; by two factors, as their
+        // product overflows for q beyond 2^116)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; x += 2)
             f2unpack(fmul2(fmul2(f2pack(sc[x2][nt][x], sc[x2][nt][x + 1]),
                                  f2pack(c_row[nt][0], c_row[nt][1])),
-                           f2pack(0x1p24f, 0x1p24f)),
+                           f2pack(scale24, scale24)),
                      sc[x2][nt][x], sc[x2][nt][x + 1]);
         load_own_token(cell + v_s<D>(0, 0, 0), va[x2], vb[x2]);
         if constexpr (kMasked) {

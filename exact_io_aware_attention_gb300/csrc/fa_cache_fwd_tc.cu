@@ -775,11 +775,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack2<kF16>(top2, big, big1);
         const bool finite = big < INFINITY && big1 < INFINITY;
         big = fmaxf(big, big1);
-        const int e = max((int)(__float_as_uint(big) >> 23), 40);
+        const int e = max((int)(__float_as_uint(big) >> 23), 11);  // (c_row is a normal number)
         const bool scaled = big > 0.f && finite;
         // (a row with an infinity or a NaN is NaN throughout: so are its scores)
         const float up = scaled ? __uint_as_float((uint32_t)(264 - e) << 23) : 1.f;
-        c_row = (scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f) * p.scale_log2;
+        c_row = scaled ? __uint_as_float((uint32_t)(e - 10) << 23) : 1.f;
         // and the sums of its groups, as two f16 terms each, for the middles of K
         const uint32_t sums = sb + L::kQx + (kNT == 2 ? t : 0) * (kRows * L::kXBytes) +
                               (r >> 3) * (8 * L::kXBytes) + (r & 7) * 16;
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           any = true;
           continue;
         }
-        const float ct = c_row * scales[(i & 3) * 4];
+        const float ct = c_row * scales[(i & 3) * 4] * p.scale_log2;
         const uint32_t found = (uint32_t)found_cells[i & 3];
         const int key0 = piece.t0 * kUnitTokens + k * kKeys;
         const bool masked = key0 + kKeys > all || found != (1u << kTileCells) - 1;

@@ -398,13 +398,14 @@ def test_non_finite_values_stay_where_they_are_seen(d, Hq):
         assert torch.equal(o, good_o) and torch.equal(lse, good_lse)
 
 
+@pytest.mark.parametrize("power", [122, -116])
 @pytest.mark.parametrize("d,Hq", [(64, 4), (128, 9), (256, 3), (64, 70), (256, 80)])
-def test_queries_near_the_largest_number(d, Hq):
-    """Scores of ordinary size from q near 2^126 and tiny keys, in place of q."""
+def test_queries_near_the_ends_of_the_exponents(d, Hq, power):
+    """Scores of ordinary size from q near 2^126 and tiny keys, or from tiny q; O in place of q."""
     L, page = 150, 32
     k, v, q = (rand((1, h, n, d), 160 + i, BF16) for i, (h, n) in
                enumerate(((1, L), (1, L), (Hq, 1))))
-    k, q = (k.float() * 2.0 ** -122).to(BF16), (q.float() * 2.0 ** 122).to(BF16)
+    k, q = (k.float() * 2.0 ** -power).to(BF16), (q.float() * 2.0 ** power).to(BF16)
     table = widen(ints([[4, 2, 0, 1, 3]]), page)
     c = new_cache(5, 1, d, page, BF16)
     fa().cache_write(c, k.cuda(), v.cuda(), table, ints([0]))
@@ -412,7 +413,7 @@ def test_queries_near_the_largest_number(d, Hq):
     qq = q.cuda()
     o2, _ = fa().cache_forward(qq, c, table, ints([L]), out=qq)
     clean()
-    compare(o, lse, q, k, v, [L], None, False, None, "large q")
+    compare(o, lse, q, k, v, [L], None, False, None, power)
     assert o2 is qq and torch.equal(o2, o.to(BF16))
 
 
